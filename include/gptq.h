@@ -16,6 +16,9 @@
  *  - gptq_w4a16_matmul multiplies activations by a packed 4-bit layer
  *    without writing the dequantized weights (section GPTQ: 4-bit weights
  *    for memory-bound decoding);
+ *  - gptq_rmsnorm_quant8, gptq_w4a8_gated and gptq_w4a8_matmul are the
+ *    feed-forward block of a decoder layer on packed layers, for any number
+ *    of tokens, with 8-bit activations between the steps;
  *  - gptq_awq_channel_scale and gptq_awq_search run the AWQ scale search
  *    (section AWQ) on the same calibration Hessian and produce 4-bit output
  *    in the same format.
@@ -28,8 +31,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default).
  *  - Calls validate their arguments first; on GPTQ_ERR_INVALID or
  *    GPTQ_ERR_WORKSPACE nothing is launched and no output is written.
- *  - gptq_hessian_accumulate, gptq_quantize_layer, gptq_w4a16_matmul and the
- *    AWQ calls are asynchronous and do not synchronize.  gptq_prepare_hinv
+ *  - gptq_hessian_accumulate, gptq_quantize_layer, gptq_w4a16_matmul, the
+ *    feed-forward calls and the AWQ calls are asynchronous and do not
+ *    synchronize.  gptq_prepare_hinv
  *    and gptq_dequant_check synchronize `stream` once to return a status /
  *    value.
  *  - Kernels never spin without bound.  A kernel whose internal wait runs out
@@ -274,6 +278,89 @@ gptq_status gptq_w4a16_matmul(const uint32_t* qweight, const float* scales,
                               const uint8_t* zeros, int64_t d_row, int64_t d_col,
                               const gptq_config* cfg, const void* X, int64_t batch,
                               float* Y, void* stream);
+
+/* Element types of the calls below. */
+typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_I8 = 2 } gptq_dtype;
+
+/* 8-bit activations, as the three calls below write and read them (the
+ * symmetric quantizer of dingiv.github.io, section 量化基础, at 8 bits):
+ *   x[t][k] = s[t][c(k)] * q[t][k],
+ *  codes   int8 n x d, token-major, row stride ldq elements, -127..127;
+ *  scales  fp32 n x n_c, row-major and dense: one per token (x_group 0,
+ *          n_c = 1) or one per token and 128 columns (x_group 128,
+ *          n_c = ceil(d / 128), the last block possibly shorter),
+ *          s = max|x| / 127, q = rint(x * (127 / max|x|)).
+ * Where the maximum is 0 the scale and the codes are 0; where it is NaN or
+ * infinite the scale is NaN and the codes are 0, so that products of that
+ * token are NaN. */
+
+/* Residual addition, root-mean-square norm and 8-bit output in one pass: what
+ * stands before the projections of a decoder layer whose linear layers are
+ * quantized (psvmc.cn page, section 大模型的分层: the norms stay in floating
+ * point).
+ *   r = X + residual, rounded once to the residual's type and stored,
+ *   y = r / sqrt(mean_k r_k^2 + eps) * weight,
+ *   codes, scales = the 8-bit form of y above.
+ * The norm is taken of the stored r.  All arithmetic is fp32.
+ *  X             n x d, row stride ldx, type x_type (GPTQ_F32 or GPTQ_BF16).
+ *  residual      n x d, row stride ldr, type r_type (GPTQ_F32 or GPTQ_BF16),
+ *                or NULL: r = X and residual_out is not written.
+ *  weight        fp32[d], or NULL for ones.  The per-channel scale of
+ *                gptq_awq_search is applied by dividing weight by s*.
+ *  eps           >= 0 and finite.
+ *  group         0 or 128, the x_group above.
+ *  residual_out  n x d, row stride ldo, type r_type; it may be X or residual
+ *                itself (same pointer, stride and type), else the arrays do
+ *                not overlap.  Ignored without a residual.
+ *  codes, ldq, scales   outputs as above; columns d .. ldq - 1 of a row are
+ *                left as they were.
+ * 0 <= n < 2^31 (n = 0 is a no-op), 1 <= d <= 65536; strides >= d; pointers
+ * aligned to their element.  Rows whose pointers and strides are multiples of
+ * 16 bytes (codes: 8) take a faster route.  Asynchronous; allocates nothing. */
+gptq_status gptq_rmsnorm_quant8(const void* X, int x_type, int64_t ldx, const void* residual,
+                                int r_type, int64_t ldr, const float* weight, double eps,
+                                int64_t n, int64_t d, int group, void* residual_out, int64_t ldo,
+                                int8_t* codes, int64_t ldq, float* scales, void* stream);
+
+/* Y = X W^T with 8-bit activations and a packed 4-bit layer, any number of
+ * tokens (dingiv.github.io page, section GPTQ: the quantized weights serve
+ * inference):
+ *   Y[t][r] = sum_k s_x[t][c(k)] x[t][k] s[r][g(k)] (q[r][k] - z[r][g(k)]).
+ *  qweight, scales, zeros, d_row, d_col, cfg   as in gptq_w4a16_matmul.
+ *  codes, ldq, x_scales, x_group   8-bit activations, n x d_col; codes
+ *             16-byte aligned, ldq >= d_col and a multiple of 16 (codes of
+ *             -128 are taken as they are).
+ *  Y          n x d_row, row stride ldy >= d_row, y_type GPTQ_F32 or
+ *             GPTQ_BF16 (rounded once); columns d_row .. ldy - 1 of a row are
+ *             left as they were.
+ * Inside a run of columns with one weight scale and one activation scale the
+ * sum is exact (whole numbers in int32); the runs' sums are scaled and added
+ * in fp32.  With runs of R = gcd(group_size, 128) columns, or 128 for
+ * group_size 0, and m = ceil(d_col / R) of them,
+ *   |Y - exact| <= (m + 16) 2^-24 sum over runs |s_x s sum_run x (q - z)|,
+ * in whatever order the runs are added.  The result does not vary from call
+ * to call; its last bits may vary with n, which decides how the sum is split.
+ * 0 <= n <= 2^24 (n = 0 is a no-op).  Asynchronous; allocates nothing. */
+gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const uint8_t* zeros,
+                             int64_t d_row, int64_t d_col, const gptq_config* cfg,
+                             const int8_t* codes, int64_t ldq, const float* x_scales, int x_group,
+                             int64_t n, void* Y, int y_type, int64_t ldy, void* stream);
+
+/* The gated pair of projections of a feed-forward block in one kernel, on two
+ * packed 4-bit layers of the same shape and configuration:
+ *   H = silu(X Wg^T) * (X Wu^T),   silu(v) = v / (1 + exp(-v)),
+ * both products as in gptq_w4a8_matmul, silu and the product in fp32.
+ *  h_type     GPTQ_F32, GPTQ_BF16, or GPTQ_I8: H as 8-bit activations with
+ *             x_group 128, which gptq_w4a8_matmul of the down projection
+ *             reads; codes to H, scales to h_scales (fp32 n x ceil(d_row /
+ *             128)).  h_scales is used for GPTQ_I8 only.
+ *  Other arguments, limits and errors as gptq_w4a8_matmul. */
+gptq_status gptq_w4a8_gated(const uint32_t* qweight_gate, const float* scales_gate,
+                            const uint8_t* zeros_gate, const uint32_t* qweight_up,
+                            const float* scales_up, const uint8_t* zeros_up, int64_t d_row,
+                            int64_t d_col, const gptq_config* cfg, const int8_t* codes,
+                            int64_t ldq, const float* x_scales, int x_group, int64_t n, void* H,
+                            int h_type, int64_t ldh, float* h_scales, void* stream);
 
 /* AWQ channel scale (dingiv.github.io "量化" page, section AWQ: salient
  * input channels are found by their mean activation magnitude):

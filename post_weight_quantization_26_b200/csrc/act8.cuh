@@ -1,0 +1,173 @@
+// Residual addition, root-mean-square norm and 8-bit output in one pass.
+//
+//   r = x + residual              (rounded once, to the residual's type, and stored)
+//   y = r * rsqrt(mean_k r_k^2 + eps) * weight
+//   s = max|y| / 127,  q = rint(y * (127 / max|y|))   per token, or per 128 columns
+//
+// The norm is taken of the stored r, so a later reader of the residual
+// stream sees the values that the codes were made from.  Everything between
+// the loads and the stores is fp32; the sum of squares is a tree over the
+// block, so its error grows with the logarithm of the row.
+//
+// Maxima are taken over the bit patterns of |y| as unsigned integers: they
+// order like the values, and every NaN lies above infinity, so a NaN is never
+// lost.  A maximum that is not finite gives the scale NaN and codes 0, which a
+// product turns into NaN for the token.  A maximum of zero gives scale 0.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace gptq {
+namespace act8 {
+
+constexpr int GROUP = 128;  // columns that share a scale, where a token has several
+
+struct Params {
+  const void* x;
+  const void* res;      // nullptr: r = x and nothing is stored
+  void* res_out;
+  const float* weight;  // nullptr: 1
+  int8_t* codes;
+  float* scales;
+  int64_t ldx, ldr, ldo, ldq;
+  int64_t n;
+  int d, n_groups;      // n_groups 1 with per-token scales
+  float eps;
+};
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float& o, float v) { o = v; }
+__device__ __forceinline__ void from_f(__nv_bfloat16& o, float v) { o = __float2bfloat16_rn(v); }
+
+// Scale and the multiplier of a maximum (given by its bits).  Maxima below
+// 2^-100 are lifted by 2^64 before the division, as 127 / max would overflow;
+// y is multiplied by `lift` first (exact for powers of two).
+struct Quant {
+  float scale, inv, lift;
+};
+__device__ __forceinline__ Quant quant_of(uint32_t top_bits) {
+  Quant q;
+  const float top = __uint_as_float(top_bits);
+  q.lift = 1.0f;
+  if (top_bits >= 0x7f800000u) {
+    q.scale = __uint_as_float(0x7fc00000u);
+    q.inv = 0.0f;
+  } else if (top == 0.0f) {
+    q.scale = q.inv = 0.0f;
+  } else {
+    q.scale = top / 127.0f;
+    if (top < 7.8886090522e-31f) q.lift = 18446744073709551616.0f;  // 2^-100, 2^64
+    q.inv = 127.0f / (top * q.lift);
+  }
+  return q;
+}
+
+// rint(y * inv) as the low byte of the sum with 1.5 * 2^23: one rounding, to
+// nearest even, at the units' place.
+__device__ __forceinline__ uint32_t code_of(float y, const Quant& q) {
+  return __float_as_uint(fmaf(y * q.lift, q.inv, 12582912.0f)) & 0xffu;
+}
+// The same with NaN and infinity in y mapped to code 0.
+__device__ __forceinline__ uint32_t code_or_zero(float y, const Quant& q) {
+  return q.inv == 0.0f ? 0u : code_of(y, q);
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float y) { return __float_as_uint(y) & 0x7fffffffu; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum (or maximum of bits) over the block; every thread gets it.  `buf` has
+// one word per warp and is free again after the next block-wide barrier.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+  v = warp_sum(v);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < warps ? buf[lane] : 0.0f);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, lane < warps ? buf[lane] : 0u);
+}
+
+// Any width, stride and alignment: one block a token, three passes that read
+// r back from where it is (the caches).  A warp owns whole groups of 128
+// columns, four a lane, and each element is only ever touched by one thread,
+// so res_out may be the memory of x or of the residual.
+template <typename TX, typename TR>
+__global__ void __launch_bounds__(256) rmsnorm_quant8_any_kernel(const Params p) {
+  __shared__ float sums[8];
+  __shared__ uint32_t tops[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  const TX* x = static_cast<const TX*>(p.x) + t * p.ldx;
+  const TR* res = p.res ? static_cast<const TR*>(p.res) + t * p.ldr : nullptr;
+  TR* out = p.res ? static_cast<TR*>(p.res_out) + t * p.ldo : nullptr;
+  const int ngr = (p.d + GROUP - 1) / GROUP;
+
+  float sum = 0.0f;
+  for (int g = warp; g < ngr; g += 8)
+    for (int j = 0; j < 4; ++j) {
+      const int k = g * GROUP + j * 32 + lane;
+      if (k < p.d) {
+        float r = to_f(x[k]);
+        if (res) {
+          TR o;
+          from_f(o, r + to_f(res[k]));
+          out[k] = o;
+          r = to_f(o);
+        }
+        sum += r * r;
+      }
+    }
+  sum = block_sum(sum, sums);
+  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+  auto value = [&](int k) {
+    const float r = res ? to_f(out[k]) : to_f(x[k]);
+    return r * rstd * (p.weight ? p.weight[k] : 1.0f);
+  };
+
+  uint32_t top = 0;
+  Quant q;
+  if (p.n_groups == 1) {
+    for (int g = warp; g < ngr; g += 8)
+      for (int j = 0; j < 4; ++j) {
+        const int k = g * GROUP + j * 32 + lane;
+        if (k < p.d) top = max(top, abs_bits(value(k)));
+      }
+    q = quant_of(block_max(top, tops));
+    if (threadIdx.x == 0) p.scales[t] = q.scale;
+  }
+  for (int g = warp; g < ngr; g += 8) {
+    float y[4];
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = g * GROUP + j * 32 + lane;
+      y[j] = k < p.d ? value(k) : 0.0f;
+      top = max(top, abs_bits(y[j]));
+    }
+    if (p.n_groups != 1) {
+      q = quant_of(__reduce_max_sync(0xffffffffu, top));
+      if (lane == 0) p.scales[t * p.n_groups + g] = q.scale;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = g * GROUP + j * 32 + lane;
+      if (k < p.d) p.codes[t * p.ldq + k] = static_cast<int8_t>(code_or_zero(y[j], q));
+    }
+  }
+}
+
+}  // namespace act8
+}  // namespace gptq

@@ -22,6 +22,8 @@
 #include "trailing_tf32.cuh"
 #include "w4a16.cuh"
 #include "awq.cuh"
+#include "act8.cuh"
+#include "w4a8.cuh"
 
 namespace {
 
@@ -447,6 +449,148 @@ gptq_status gptq_w4a16_matmul(const uint32_t* qweight, const float* scales,
 #undef GPTQ_W4
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
+}
+
+gptq_status gptq_rmsnorm_quant8(const void* X, int x_type, int64_t ldx, const void* residual,
+                                int r_type, int64_t ldr, const float* weight, double eps,
+                                int64_t n, int64_t d, int group, void* residual_out, int64_t ldo,
+                                int8_t* codes, int64_t ldq, float* scales, void* stream) {
+  if (n < 0 || n > INT32_MAX || d < 1 || d > 65536 || (group != 0 && group != act8::GROUP))
+    return GPTQ_ERR_INVALID;
+  const float eps_f = static_cast<float>(eps);
+  if (!(eps >= 0.0) || !std::isfinite(eps_f)) return GPTQ_ERR_INVALID;
+  if (x_type != GPTQ_F32 && x_type != GPTQ_BF16) return GPTQ_ERR_INVALID;
+  if (residual && r_type != GPTQ_F32 && r_type != GPTQ_BF16) return GPTQ_ERR_INVALID;
+  if (ldx < d || ldq < d || (residual && (ldr < d || ldo < d))) return GPTQ_ERR_INVALID;
+  if (n == 0) return GPTQ_OK;
+  if (!X || !codes || !scales || (residual && !residual_out)) return GPTQ_ERR_INVALID;
+  const size_t xb = x_type == GPTQ_F32 ? 4 : 2, rb = r_type == GPTQ_F32 ? 4 : 2;
+  if (!aligned(X, xb) || !aligned(scales, 4) || !aligned(weight, 4) ||
+      (residual && (!aligned(residual, rb) || !aligned(residual_out, rb))))
+    return GPTQ_ERR_INVALID;
+  act8::Params p{};
+  p.x = X;
+  p.res = residual;
+  p.res_out = residual_out;
+  p.weight = weight;
+  p.codes = codes;
+  p.scales = scales;
+  p.ldx = ldx;
+  p.ldr = ldr;
+  p.ldo = ldo;
+  p.ldq = ldq;
+  p.n = n;
+  p.d = static_cast<int>(d);
+  p.n_groups = group ? (p.d + act8::GROUP - 1) / act8::GROUP : 1;
+  p.eps = eps_f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(n);
+  const bool xf = x_type == GPTQ_F32, rf = r_type == GPTQ_F32;
+  if (xf && rf) act8::rmsnorm_quant8_any_kernel<float, float><<<grid, 256, 0, s>>>(p);
+  else if (xf) act8::rmsnorm_quant8_any_kernel<float, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  else if (rf) act8::rmsnorm_quant8_any_kernel<__nv_bfloat16, float><<<grid, 256, 0, s>>>(p);
+  else act8::rmsnorm_quant8_any_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool w4a8_layer_ok(const uint32_t* qweight, const float* scales, const uint8_t* zeros) {
+  return qweight && scales && zeros && aligned(qweight, 16) && aligned(scales, 4);
+}
+
+// Both products: the arguments' checks and the launch.  `p` brings the layers.
+template <bool GATED>
+gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gptq_config* cfg,
+                         const int8_t* codes, int64_t ldq, const float* x_scales, int x_group,
+                         int64_t n, void* y, int y_type, int64_t ldy, float* y_scales,
+                         void* stream) {
+  if (d_row < 1 || d_row > (int64_t(1) << 24) || d_col < 32 || d_col % 32 != 0 || d_col > 65536)
+    return GPTQ_ERR_INVALID;
+  if (!config_ok(cfg, d_col) || cfg->bits != 4) return GPTQ_ERR_INVALID;
+  if (n < 0 || n > (int64_t(1) << 24) || (x_group != 0 && x_group != act8::GROUP))
+    return GPTQ_ERR_INVALID;
+  if (y_type != GPTQ_F32 && y_type != GPTQ_BF16 && !(GATED && y_type == GPTQ_I8))
+    return GPTQ_ERR_INVALID;
+  if (ldq < d_col || ldq % 16 != 0 || ldy < d_row) return GPTQ_ERR_INVALID;
+  for (int i = 0; i < (GATED ? 2 : 1); ++i)
+    if (!w4a8_layer_ok(p.layer[i].qweight, p.layer[i].scales, p.layer[i].zeros))
+      return GPTQ_ERR_INVALID;
+  if (n == 0) return GPTQ_OK;
+  if (!codes || !x_scales || !y || !aligned(codes, 16) || !aligned(x_scales, 4))
+    return GPTQ_ERR_INVALID;
+  if (!aligned(y, y_type == GPTQ_F32 ? 4 : y_type == GPTQ_BF16 ? 2 : 1)) return GPTQ_ERR_INVALID;
+  if (y_type == GPTQ_I8 && (!y_scales || !aligned(y_scales, 4))) return GPTQ_ERR_INVALID;
+  p.x = codes;
+  p.xs = x_scales;
+  p.y = y;
+  p.ys = y_scales;
+  p.ldx = ldq;
+  p.ldy = ldy;
+  p.n = n;
+  p.d_row = static_cast<int>(d_row);
+  p.d_col = static_cast<int>(d_col);
+  p.group = cfg->group_size ? cfg->group_size : p.d_col;
+  p.n_groups = p.d_col / p.group;
+  p.xgroups = x_group ? (p.d_col + 127) / 128 : 1;
+  p.out = y_type;
+
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute at[1];
+  const unsigned tiles = static_cast<unsigned>((p.d_row + w4a8::ROWS - 1) / w4a8::ROWS);
+  const unsigned ctas = (tiles + w4a8::CLUSTER - 1) / w4a8::CLUSTER * w4a8::CLUSTER;
+  const unsigned toks = static_cast<unsigned>((n + w4a8::TOK - 1) / w4a8::TOK);
+  if (toks > 65535) return GPTQ_ERR_INVALID;
+  lc.gridDim = dim3(y_type == GPTQ_I8 ? ctas : tiles, toks);
+  lc.blockDim = dim3(w4a8::THREADS);
+  lc.stream = static_cast<cudaStream_t>(stream);
+  if (y_type == GPTQ_I8) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = w4a8::CLUSTER;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+  }
+  const int g = p.group;
+  // a region of 32 RJ columns has one scale: with one scale a row, always;
+  // else it must lie inside a group
+  cudaError_t e;
+  if (p.n_groups == 1 || g % 128 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 4>, p);
+  else if (g % 64 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 2>, p);
+  else e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 1>, p);
+  (void)e;  // sticky until cudaGetLastError, which the check reads
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const uint8_t* zeros,
+                             int64_t d_row, int64_t d_col, const gptq_config* cfg,
+                             const int8_t* codes, int64_t ldq, const float* x_scales, int x_group,
+                             int64_t n, void* Y, int y_type, int64_t ldy, void* stream) {
+  w4a8::Params p{};
+  p.layer[0] = w4a8::Layer{qweight, scales, zeros};
+  return w4a8_product<false>(p, d_row, d_col, cfg, codes, ldq, x_scales, x_group, n, Y, y_type,
+                             ldy, nullptr, stream);
+}
+
+gptq_status gptq_w4a8_gated(const uint32_t* qweight_gate, const float* scales_gate,
+                            const uint8_t* zeros_gate, const uint32_t* qweight_up,
+                            const float* scales_up, const uint8_t* zeros_up, int64_t d_row,
+                            int64_t d_col, const gptq_config* cfg, const int8_t* codes,
+                            int64_t ldq, const float* x_scales, int x_group, int64_t n, void* H,
+                            int h_type, int64_t ldh, float* h_scales, void* stream) {
+  w4a8::Params p{};
+  p.layer[0] = w4a8::Layer{qweight_gate, scales_gate, zeros_gate};
+  p.layer[1] = w4a8::Layer{qweight_up, scales_up, zeros_up};
+  return w4a8_product<true>(p, d_row, d_col, cfg, codes, ldq, x_scales, x_group, n, H, h_type,
+                            ldh, h_scales, stream);
 }
 
 gptq_status gptq_awq_channel_scale(const void* X, int64_t n, int64_t d, int64_t ldx, double* sx,

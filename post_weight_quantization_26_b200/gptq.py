@@ -27,8 +27,11 @@ EXPORTED = ("gptq_workspace_size", "gptq_hessian_accumulate",
             "gptq_prepare_factor", "gptq_quantize_layer_factor",
             "gptq_device_status", "gptq_status_string", "gptq_launch_count",
             "gptq_dequant_check_noalloc", "gptq_w4a16_matmul", "gptq_awq_channel_scale",
-            "gptq_awq_workspace_size", "gptq_awq_search")
+            "gptq_awq_workspace_size", "gptq_awq_search",
+            "gptq_rmsnorm_quant8", "gptq_w4a8_matmul", "gptq_w4a8_gated")
 NOALLOC_MAX_TILES = 65536  # GPTQ_NOALLOC_MAX_TILES in include/gptq.h
+ACT_GROUP = 128  # columns that share an activation scale, where a token has several
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.int8: 2}  # gptq_dtype in include/gptq.h
 FAULT_NONE, FAULT_SYRK_STALL, FAULT_TRAILING_STALL = 0, 1, 2  # GPTQ_FAULT_* in include/gptq.h
 
 
@@ -91,6 +94,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gptq_dequant_check_noalloc.restype = I
     lib.gptq_w4a16_matmul.argtypes = [P, P, P, I64, I64, cfgp, P, I64, P, P]
     lib.gptq_w4a16_matmul.restype = I
+    lib.gptq_rmsnorm_quant8.argtypes = [P, I, I64, P, I, I64, P, D, I64, I64, I, P, I64, P, I64,
+                                        P, P]
+    lib.gptq_rmsnorm_quant8.restype = I
+    lib.gptq_w4a8_matmul.argtypes = [P, P, P, I64, I64, cfgp, P, I64, P, I, I64, P, I, I64, P]
+    lib.gptq_w4a8_matmul.restype = I
+    lib.gptq_w4a8_gated.argtypes = [P, P, P, P, P, P, I64, I64, cfgp, P, I64, P, I, I64, P, I,
+                                    I64, P, P]
+    lib.gptq_w4a8_gated.restype = I
     lib.gptq_awq_channel_scale.argtypes = [P, I64, I64, I64, P, P]
     lib.gptq_awq_channel_scale.restype = I
     lib.gptq_awq_workspace_size.argtypes = [I64, I64, cfgp]
@@ -278,6 +289,165 @@ def gptq_w4a16_matmul(qweight, scales, zeros, cfg: GptqConfig, X, Y=None,
         ctypes.byref(cfg), _ptr(X), batch, _ptr(Y), _stream(stream))
     _check(st, "gptq_w4a16_matmul")
     return Y
+
+
+def _elsewhere(t, stream):
+    """None where a call on tensor t runs on the current stream of t's device
+    and that device is current; else the context to make the call in.  Outputs
+    that the call allocates then belong to the stream that it runs on."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+
+
+def _one_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _rows(name, t, dtypes, shape):
+    """The row stride of a matrix of a given shape whose rows are dense."""
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtypes} {tuple(shape)}")
+    n, d = shape
+    if (d > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < d):
+        raise ValueError(f"{name}: rows must be dense, strides {t.stride()}")
+    return t.stride(0) if n > 1 else max(d, t.stride(0))
+
+
+def _dense(name, t, dtypes, shape):
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous {dtypes} "
+                         f"{tuple(shape)}")
+
+
+def alloc_codes(n: int, d: int, group: int = ACT_GROUP, device="cuda"):
+    """8-bit activations n x d: int8 codes (row stride a multiple of 16, as
+    the products need it) and fp32 scales."""
+    codes = torch.empty((n, (d + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :d]
+    return codes, torch.empty((n, -(-d // group) if group else 1), dtype=torch.float32,
+                              device=device)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def gptq_rmsnorm_quant8(X, weight, eps: float = 1e-6, residual=None, group: int = ACT_GROUP,
+                        residual_out=None, out=None, stream=None):
+    """r = X + residual (stored in the residual's type), y = r / sqrt(mean r^2
+    + eps) * weight, y as int8 codes and scales (one per token for group 0, one
+    per token and 128 columns for group 128).  X and residual are n x d, fp32
+    or bf16 each; weight is fp32[d] or None.  Returns (codes, scales), and r
+    as a third where a residual is given; `out` = (codes, scales) and
+    `residual_out` are allocated where they are not given, and residual_out
+    may be the residual itself."""
+    place = _elsewhere(X, stream)
+    if place is not None:
+        with place:
+            return gptq_rmsnorm_quant8(X, weight, eps, residual, group, residual_out, out)
+    if X.dim() != 2:
+        raise ValueError("X must be n x d")
+    n, d = X.shape
+    codes, scales = alloc_codes(n, d, group, X.device) if out is None else out
+    _one_device(X, weight, residual, residual_out, codes, scales)
+    ldx = _rows("X", X, _FLOATS, (n, d))
+    ldq = _rows("codes", codes, (torch.int8,), (n, d))
+    _dense("scales", scales, (torch.float32,), (n, -(-d // ACT_GROUP) if group else 1))
+    if weight is not None:
+        _dense("weight", weight, (torch.float32,), (d,))
+    r_type = ldr = ldo = 0
+    if residual is not None:
+        if residual_out is None:
+            residual_out = torch.empty((n, d), dtype=residual.dtype, device=X.device)
+        ldr = _rows("residual", residual, _FLOATS, (n, d))
+        ldo = _rows("residual_out", residual_out, (residual.dtype,), (n, d))
+        r_type = DTYPES[residual.dtype]
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    st = load_library().gptq_rmsnorm_quant8(
+        X.data_ptr(), DTYPES[X.dtype], ldx, None if residual is None else residual.data_ptr(),
+        r_type, ldr, None if weight is None else weight.data_ptr(), eps, n, d, group,
+        None if residual is None else residual_out.data_ptr(), ldo, codes.data_ptr(), ldq,
+        scales.data_ptr(), _stream(None))
+    _check(st, "gptq_rmsnorm_quant8")
+    return (codes, scales) if residual is None else (codes, scales, residual_out)
+
+
+def _w4a8_args(layers, cfg, codes, x_scales):
+    """Checks what both products share; returns (n, d_row, d_col, ldq, x_group)."""
+    if codes.dim() != 2:
+        raise ValueError("codes must be n x d_col")
+    n, d_col = codes.shape
+    ldq = _rows("codes", codes, (torch.int8,), (n, d_col))
+    if n <= 1:
+        ldq = (ldq + 15) // 16 * 16  # the stride of one row is not used
+    blocks = -(-d_col // ACT_GROUP)
+    x_group = 0 if x_scales.dim() == 2 and x_scales.shape[1] == 1 else ACT_GROUP
+    _dense("x_scales", x_scales, (torch.float32,), (n, blocks if x_group else 1))
+    d_row = layers[0][1].shape[0]
+    _one_device(codes, x_scales, *(t for layer in layers for t in layer))
+    ng = n_groups(d_col, cfg.group_size)
+    for qweight, scales, zeros in layers:
+        _dense("qweight", qweight, (torch.int32, torch.uint32), (d_row, d_col // 8))
+        _dense("scales", scales, (torch.float32,), (d_row, ng))
+        _dense("zeros", zeros, (torch.uint8,), (d_row, ng))
+    return n, d_row, d_col, ldq, x_group
+
+
+def gptq_w4a8_matmul(qweight, scales, zeros, cfg: GptqConfig, codes, x_scales, Y=None,
+                     dtype=torch.float32, stream=None):
+    """Y = X W^T for 8-bit activations (codes int8 n x d_col and x_scales, as
+    gptq_rmsnorm_quant8 and gptq_w4a8_gated write them) and a packed 4-bit
+    layer.  Y is n x d_row, fp32 or bf16, allocated in `dtype` when not given.
+    Returns Y."""
+    place = _elsewhere(codes, stream)
+    if place is not None:
+        with place:
+            return gptq_w4a8_matmul(qweight, scales, zeros, cfg, codes, x_scales, Y, dtype)
+    n, d_row, d_col, ldq, x_group = _w4a8_args([(qweight, scales, zeros)], cfg, codes, x_scales)
+    if Y is None:
+        Y = torch.empty((n, d_row), dtype=dtype, device=codes.device)
+    _one_device(codes, Y)
+    ldy = _rows("Y", Y, _FLOATS, (n, d_row))
+    st = load_library().gptq_w4a8_matmul(
+        qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), d_row, d_col, ctypes.byref(cfg),
+        codes.data_ptr(), ldq, x_scales.data_ptr(), x_group, n, Y.data_ptr(), DTYPES[Y.dtype], ldy,
+        _stream(None))
+    _check(st, "gptq_w4a8_matmul")
+    return Y
+
+
+def gptq_w4a8_gated(gate, up, cfg: GptqConfig, codes, x_scales, out=None, dtype=torch.bfloat16,
+                    stream=None):
+    """H = silu(X Wg^T) * (X Wu^T) for 8-bit activations and two packed 4-bit
+    layers, each (qweight, scales, zeros).  dtype float32 or bfloat16: returns
+    H (n x d_row), which `out` may give; int8: returns H as (codes, scales)
+    with a scale per token and 128 columns, which `out` may give as a pair."""
+    place = _elsewhere(codes, stream)
+    if place is not None:
+        with place:
+            return gptq_w4a8_gated(gate, up, cfg, codes, x_scales, out, dtype)
+    n, d_row, d_col, ldq, x_group = _w4a8_args([gate, up], cfg, codes, x_scales)
+    if out is None:
+        out = (alloc_codes(n, d_row, ACT_GROUP, codes.device) if dtype == torch.int8 else
+               torch.empty((n, d_row), dtype=dtype, device=codes.device))
+    H, h_scales = out if isinstance(out, (tuple, list)) else (out, None)
+    _one_device(codes, H, h_scales)
+    ldh = _rows("H", H, _FLOATS if h_scales is None else (torch.int8,), (n, d_row))
+    if h_scales is not None:
+        _dense("h_scales", h_scales, (torch.float32,), (n, -(-d_row // ACT_GROUP)))
+    st = load_library().gptq_w4a8_gated(
+        gate[0].data_ptr(), gate[1].data_ptr(), gate[2].data_ptr(), up[0].data_ptr(),
+        up[1].data_ptr(), up[2].data_ptr(), d_row, d_col, ctypes.byref(cfg), codes.data_ptr(), ldq,
+        x_scales.data_ptr(), x_group, n, H.data_ptr(), DTYPES[H.dtype], ldh,
+        None if h_scales is None else h_scales.data_ptr(), _stream(None))
+    _check(st, "gptq_w4a8_gated")
+    return out
 
 
 def gptq_awq_channel_scale(X, sx=None, stream=None):
