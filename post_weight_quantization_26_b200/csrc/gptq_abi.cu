@@ -24,6 +24,7 @@
 #include "awq.cuh"
 #include "act8.cuh"
 #include "w4a8.cuh"
+#include "w4a8_tiled.cuh"
 
 namespace {
 
@@ -85,6 +86,29 @@ struct DeviceInfo {
   std::mutex qmu;
 };
 
+// Tile shapes of the W4A8 products (w4a8_tiled.cuh): layers, tokens, epilogue
+// warps, ring stages, operand slots, CTAs per SM, persistent.
+template <bool GATED>
+struct W4a8Cfg {
+  static constexpr int NL = GATED ? 2 : 1;
+  using Tiny = w4a8t::Cfg<NL, 16, 4, GATED ? 3 : 5, GATED ? 3 : 2, 2, false>;
+  using Small = w4a8t::Cfg<NL, 64 / NL, 4, GATED ? 3 : 4, GATED ? 3 : 2, 2, false>;
+  using Mid = w4a8t::Cfg<NL, 128 / NL, 8, 5, GATED ? 4 : 3, 1, false>;
+  using Big = w4a8t::Cfg<NL, 256 / NL, 8, 4, GATED ? 4 : 3, 1, true>;
+};
+
+// The shared memory of a tile kernel, and the carveout that lets MINB CTAs of
+// it share an SM.
+template <class C>
+cudaError_t w4a8_allow_smem() {
+  const auto f = w4a8t::w4a8_tiled_kernel<C>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared);
+}
+
 std::mutex g_mu;
 DeviceInfo g_dev[64];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -111,6 +135,14 @@ gptq_status device_setup(int* num_sms) {
                           reinterpret_cast<const void*>(w4a16::w4a16_matmul_kernel<1, 1>)})
       GPTQ_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          w4a16::WARPS * w4a16::WARP_BUDGET + w4a16::RED_BYTES));
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Tiny>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Small>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Mid>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Big>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Tiny>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Small>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Mid>());
+    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Big>());
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(syrk::syrk_bf16_tcgen05_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        syrk::SMEM_BYTES));
@@ -502,6 +534,107 @@ bool w4a8_layer_ok(const uint32_t* qweight, const float* scales, const uint8_t* 
   return qweight && scales && zeros && aligned(qweight, 16) && aligned(scales, 4);
 }
 
+// 2-D byte matrix for TMA: rows of `inner` bytes, box bx x by.
+gptq_status encode_u8_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
+                         uint64_t row_bytes, uint32_t bx, uint32_t by, CUtensorMapSwizzle swz) {
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {bx, by};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult cr = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS) {
+    std::fprintf(stderr, "gptq: cuTensorMapEncodeTiled (u8) failed (%d)\n", static_cast<int>(cr));
+    return GPTQ_ERR_CUDA;
+  }
+  return GPTQ_OK;
+}
+
+// Few tokens: one launch of the row kernel.
+template <bool GATED>
+gptq_status w4a8_rows(const w4a8::Params& p, cudaStream_t s) {
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute at[1];
+  const unsigned tiles = static_cast<unsigned>((p.d_row + w4a8::ROWS - 1) / w4a8::ROWS);
+  const unsigned ctas = (tiles + w4a8::CLUSTER - 1) / w4a8::CLUSTER * w4a8::CLUSTER;
+  const unsigned toks = static_cast<unsigned>((p.n + w4a8::TOK - 1) / w4a8::TOK);
+  lc.gridDim = dim3(p.out == GPTQ_I8 ? ctas : tiles, toks);
+  lc.blockDim = dim3(w4a8::THREADS);
+  lc.stream = s;
+  if (p.out == GPTQ_I8) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = w4a8::CLUSTER;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+  }
+  const int g = p.group;
+  // a region of 32 RJ columns has one scale: with one scale a row, always;
+  // else it must lie inside a group
+  cudaError_t e;
+  if (p.n_groups == 1 || g % 128 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 4>, p);
+  else if (g % 64 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 2>, p);
+  else e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 1>, p);
+  (void)e;  // also kept for cudaGetLastError, which the check reads
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
+template <class C>
+int64_t w4a8_tiles(const w4a8::Params& p) {
+  return ((p.d_row + w4a8t::BM - 1) / w4a8t::BM) * ((p.n + C::TN - 1) / C::TN);
+}
+
+template <class C>
+gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
+  w4a8t::Tiled a{};
+  a.p = p;
+  a.row_tiles = (p.d_row + w4a8t::BM - 1) / w4a8t::BM;
+  a.tok_tiles = static_cast<int>((p.n + C::TN - 1) / C::TN);
+  const int64_t tiles = w4a8_tiles<C>(p);
+  const int nchunks = (p.d_col + w4a8t::CH - 1) / w4a8t::CH;
+  a.runs = p.n_groups == 1 || p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
+  a.wait_ns = g_wait_ns.load();
+  a.ksplit = 1;
+  if (!C::BIG) {
+    // The split that ends first: rounds of CTAs, each its chunks and a ramp
+    // worth about six chunks (launch, first loads, the sums' exchange).
+    const int64_t slots = static_cast<int64_t>(num_sms) * C::MINB;
+    int64_t best = INT64_MAX;
+    for (int k = 1; k <= 8 && k <= nchunks; k *= 2) {
+      const int64_t cost = ((tiles * k + slots - 1) / slots) * ((nchunks + k - 1) / k + 6);
+      if (cost < best) { best = cost; a.ksplit = k; }
+    }
+  }
+  CUtensorMap mw[2], mx;
+  for (int l = 0; l < 2; ++l) {
+    gptq_status st = encode_u8_2d(&mw[l], p.layer[l < C::NL ? l : 0].qweight, p.d_col / 2, p.d_row,
+                                  p.d_col / 2, w4a8t::CH / 2, w4a8t::BM, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (st != GPTQ_OK) return st;
+  }
+  gptq_status st = encode_u8_2d(&mx, p.x, p.d_col, p.n, p.ldx, w4a8t::CH, C::TN,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != GPTQ_OK) return st;
+  cudaLaunchConfig_t lc{};
+  cudaLaunchAttribute at[1];
+  if (!C::BIG && tiles * a.ksplit > INT32_MAX) return GPTQ_ERR_INVALID;
+  lc.gridDim = dim3(static_cast<unsigned>(C::BIG ? std::min<int64_t>(tiles, num_sms)
+                                                 : tiles * a.ksplit));
+  lc.blockDim = dim3(C::THREADS);
+  lc.dynamicSmemBytes = C::SMEM;
+  lc.stream = s;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.ksplit;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&lc, w4a8t::w4a8_tiled_kernel<C>, mw[0], mw[1], mx, a);
+  (void)e;  // also kept for cudaGetLastError, which the check reads
+  GPTQ_LAUNCH_CHECK();
+  return GPTQ_OK;
+}
+
 // Both products: the arguments' checks and the launch.  `p` brings the layers.
 template <bool GATED>
 gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gptq_config* cfg,
@@ -538,32 +671,17 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
   p.xgroups = x_group ? (p.d_col + 127) / 128 : 1;
   p.out = y_type;
 
-  cudaLaunchConfig_t lc{};
-  cudaLaunchAttribute at[1];
-  const unsigned tiles = static_cast<unsigned>((p.d_row + w4a8::ROWS - 1) / w4a8::ROWS);
-  const unsigned ctas = (tiles + w4a8::CLUSTER - 1) / w4a8::CLUSTER * w4a8::CLUSTER;
-  const unsigned toks = static_cast<unsigned>((n + w4a8::TOK - 1) / w4a8::TOK);
-  if (toks > 65535) return GPTQ_ERR_INVALID;
-  lc.gridDim = dim3(y_type == GPTQ_I8 ? ctas : tiles, toks);
-  lc.blockDim = dim3(w4a8::THREADS);
-  lc.stream = static_cast<cudaStream_t>(stream);
-  if (y_type == GPTQ_I8) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = w4a8::CLUSTER;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-  }
-  const int g = p.group;
-  // a region of 32 RJ columns has one scale: with one scale a row, always;
-  // else it must lie inside a group
-  cudaError_t e;
-  if (p.n_groups == 1 || g % 128 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 4>, p);
-  else if (g % 64 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 2>, p);
-  else e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 1>, p);
-  (void)e;  // sticky until cudaGetLastError, which the check reads
-  GPTQ_LAUNCH_CHECK();
-  return GPTQ_OK;
+  int num_sms = 148;
+  gptq_status st = device_setup(&num_sms);
+  if (st != GPTQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n <= w4a8::TOK) return w4a8_rows<GATED>(p, s);
+  using Cf = W4a8Cfg<GATED>;
+  if (n <= Cf::Tiny::TN) return w4a8_tiled<typename Cf::Tiny>(p, num_sms, s);
+  if (n <= Cf::Small::TN) return w4a8_tiled<typename Cf::Small>(p, num_sms, s);
+  const int64_t big = w4a8_tiles<typename Cf::Big>(p);
+  if (n > Cf::Mid::TN && big >= num_sms) return w4a8_tiled<typename Cf::Big>(p, num_sms, s);
+  return w4a8_tiled<typename Cf::Mid>(p, num_sms, s);
 }
 
 }  // namespace

@@ -1,0 +1,551 @@
+// Products with packed 4-bit layers and 8-bit activations on the 5th-generation
+// tensor cores, for more than a few tokens.  The mathematics is that of
+// w4a8.cuh; here the zero points are subtracted from the codes on the way into
+// shared memory, so a run's sum comes out of one contraction of signed bytes
+// (kind::i8, int32 accumulators, exact).
+//
+// A tile is 128 rows of the layer (of both layers, for the gated pair) by TN
+// tokens.  The layer's rows are the M side, so the weight scale of a run is one
+// value a thread in the epilogue, and the tokens' scales are broadcast reads.
+// Work goes in chunks of 128 columns:
+//
+//   TMA warp      packed rows (64 B a row and chunk, 64-byte swizzle) and the
+//                 tokens' codes (128 B, 128-byte swizzle) into a ring
+//   unpack warps  a thread has a row: words of eight codes -> q - z as signed
+//                 bytes in column order, into 128-byte-swizzled operand slots.
+//                 Bytes 0x80 + q - z never borrow from their neighbour, so four
+//                 codes cost an AND-OR, a subtraction, half of two PRMT, an XOR
+//   MMA warp      one thread issues tcgen05.mma, 32 columns each; a run (32, 64
+//                 or 128 columns, or more where no scale changes) starts from
+//                 zero in its own TMEM buffer
+//   epilogue      int32 -> fp32, times weight scale and token scale, added to
+//                 fp32 registers while the next runs are in the tensor cores
+//
+// Every mbarrier wait is bounded, as in the Hessian kernel.
+//
+// Three shapes (Cfg): SMALL and MID have one tile a cluster of up to 8 CTAs
+// that split the chunks; their sums meet in shared memory of the cluster, in
+// rank order, so the result does not vary.  BIG is persistent, without a split.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "w4a8.cuh"
+
+namespace gptq {
+namespace w4a8t {
+
+using w4a8::Params;
+
+constexpr int BM = 128;  // layer rows per tile
+constexpr int CH = 128;  // columns per chunk
+constexpr int PACKED_BYTES = BM * CH / 2;
+constexpr int SLOT_BYTES = BM * CH;
+
+// TN_: tokens per tile; EW_: epilogue warps; S_: ring stages; AS_: operand
+// slots of one layer and chunk; MINB: CTAs per SM.
+template <int NL_, int TN_, int EW_, int S_, int AS_, int MINB_, bool BIG_>
+struct Cfg {
+  static constexpr int NL = NL_, TN = TN_, EW = EW_, S = S_, AS = AS_, MINB = MINB_;
+  static constexpr bool BIG = BIG_;
+  static constexpr int UW = 4;                       // unpack warps
+  static constexpr int WARPS = BIG ? 16 : UW + EW + 2;  // BIG: whole warpgroups
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int NU = 512 / MINB / TN < 4 ? 512 / MINB / TN : 4;  // TMEM buffers
+  static constexpr int TMEM_COLS = NU * TN;
+  static constexpr int COLS = TN / (EW / 4);         // columns (tokens) per epilogue warp
+  static constexpr int X_BYTES = TN * CH;
+  static constexpr int STAGE_BYTES = NL * PACKED_BYTES + X_BYTES;
+  static constexpr int RING_BYTES = S * STAGE_BYTES;
+  static constexpr int SUM_BYTES = BIG ? 0 : NL * TN * BM * 4;  // over the ring, at the end
+  static constexpr int SX_BYTES = 2 * TN * 4;
+  static constexpr int TOP_BYTES = BIG ? 4 * TN * 4 : 0;
+  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 1;
+  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + TOP_BYTES + BARS * 8 + 16 +
+                              1024 /* alignment */;
+  static_assert(NU >= NL && TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
+  static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
+  static_assert(EW * 32 >= TN && COLS % 16 == 0, "epilogue threads");
+  static_assert(!BIG || TN * NL == 256, "registers");
+};
+
+struct Tiled {
+  Params p;
+  int row_tiles, tok_tiles;
+  int ksplit;        // CTAs of a cluster along the columns
+  int runs;          // runs per chunk: 4 (32 columns), 2, or 1
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Four signed bytes q - z of one word's even or odd codes, still biased by 128.
+__device__ __forceinline__ uint32_t biased(uint32_t codes, uint32_t z4) {
+  return ((codes & 0x0F0F0F0Fu) | 0x80808080u) - z4;
+}
+
+// Eight codes of a word -> eight signed bytes in column order.
+__device__ __forceinline__ uint2 unpack_word(uint32_t w, uint32_t z4) {
+  const uint32_t lo = biased(w, z4), hi = biased(w >> 4, z4);
+  return make_uint2(__byte_perm(lo, hi, 0x5140) ^ 0x80808080u,
+                    __byte_perm(lo, hi, 0x7362) ^ 0x80808080u);
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::MINB)
+w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
+                  const __grid_constant__ CUtensorMap tmap_w1,
+                  const __grid_constant__ CUtensorMap tmap_x, const Tiled a) {
+  constexpr int NL = C::NL, TN = C::TN, S = C::S, AS = C::AS, NU = C::NU, EW = C::EW, UW = C::UW;
+  constexpr uint32_t IDESC = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(TN >> 3) << 17) |
+                             (uint32_t(BM >> 4) << 24);  // s32 += s8 x s8, both K-major
+  namespace cg = cooperative_groups;
+  const Params& p = a.p;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (ring - raw);
+  const uint32_t slots = ring + C::RING_BYTES;
+  float* sx = reinterpret_cast<float*>(base + C::RING_BYTES + AS * SLOT_BYTES);
+  uint32_t* tops = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sx) + C::SX_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, afull0 = empty0 + 8u * S,
+                 aempty0 = afull0 + 8u * AS, tfull0 = aempty0 + 8u * AS,
+                 tempty0 = tfull0 + 8u * NU, drain = tempty0 + 8u * NU;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, UW + 1);  // unpacked, and multiplied
+    }
+    for (int s = 0; s < AS; ++s) {
+      mbar_init(afull0 + 8u * s, UW);
+      mbar_init(aempty0 + 8u * s, 1);
+    }
+    for (int u = 0; u < NU; ++u) {
+      mbar_init(tfull0 + 8u * u, 1);
+      mbar_init(tempty0 + 8u * u, EW);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tmap_w0);
+    if (NL == 2) tma_prefetch_desc(&tmap_w1);
+    tma_prefetch_desc(&tmap_x);
+  }
+  if (warp == UW + EW + 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int nchunks = (p.d_col + CH - 1) / CH;
+  const int krank = C::BIG ? 0 : static_cast<int>(blockIdx.x) % a.ksplit;
+  const int c0 = static_cast<int>(static_cast<int64_t>(nchunks) * krank / a.ksplit);
+  const int c1 = static_cast<int>(static_cast<int64_t>(nchunks) * (krank + 1) / a.ksplit);
+  const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.tok_tiles;
+  const int64_t tile0 = C::BIG ? blockIdx.x : blockIdx.x / a.ksplit;
+  const int64_t tile_step = C::BIG ? gridDim.x : tiles;
+  // a chunk's last run closes its TMEM buffer unless neither scale changes
+  auto closes = [&](int c) {
+    return c == c1 - 1 || p.xgroups != 1 || a.runs != 1 ||
+           (p.n_groups != 1 && ((c + 1) * CH) % p.group == 0);
+  };
+  bool ok = true;
+#define W4T_WAIT(bar, par) \
+  (ok = ok && mbar_wait_bounded((bar), (par), abort_flag, a.wait_ns))
+
+  // BIG: 65536 registers at launch, 512 x 128 = 256 x 200 (epilogue) + 256 x 56
+#define W4T_FEWER() \
+  if (C::BIG) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;")
+#define W4T_MORE() \
+  if (C::BIG) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;")
+
+  if (warp >= UW + EW) {
+    W4T_FEWER();  // the whole warpgroup, at one place
+    if (warp == UW + EW) {
+      // ------------------------------------------------------------ TMA warp
+      if (lane == 0) {
+        uint32_t st = 0, ph = 0, issued = 0;
+        for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
+          const int row = static_cast<int>(t / a.tok_tiles) * BM;
+          const int tok = static_cast<int>(t % a.tok_tiles) * TN;
+          for (int c = c0; c < c1; ++c) {
+            if (!W4T_WAIT(empty0 + 8u * st, ph ^ 1u)) break;
+            const uint32_t fb = full0 + 8u * st, at = ring + st * C::STAGE_BYTES;
+            mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+            tma_load_2d(at, &tmap_w0, fb, c * (CH / 2), row);
+            if (NL == 2) tma_load_2d(at + PACKED_BYTES, &tmap_w1, fb, c * (CH / 2), row);
+            tma_load_2d(at + NL * PACKED_BYTES, &tmap_x, fb, c * CH, tok);
+            ++issued;
+            if (++st == S) { st = 0; ph ^= 1u; }
+          }
+        }
+        if (!ok) {  // given up: no copy may land in memory that is handed on
+          int own = 0;
+          for (uint32_t k = 0; k < S && k < issued; ++k) {
+            const uint32_t i = issued - 1 - k;
+            mbar_wait_bounded(full0 + 8u * (i % S), (i / S) & 1u, &own, a.wait_ns);
+          }
+        }
+      }
+    } else if (warp == UW + EW + 1) {
+      // ------------------------------------------------------------ MMA warp
+      if (lane == 0) {
+        uint32_t st = 0, ph = 0, slot = 0, sph = 0, unit = 0;
+        bool open = false;  // the current buffers hold a started run
+        for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
+          for (int c = c0; c < c1 && ok; ++c) {
+            if (!W4T_WAIT(full0 + 8u * st, ph)) break;
+            const uint32_t xb = ring + st * C::STAGE_BYTES + NL * PACKED_BYTES;
+            const bool close = closes(c);
+            const int nmma = 4 / a.runs;
+            for (int l = 0; l < NL && ok; ++l) {
+              if (!W4T_WAIT(afull0 + 8u * slot, sph)) break;
+              tc_fence_after();
+              const uint32_t ab = slots + slot * SLOT_BYTES;
+              for (int m = 0; m < a.runs; ++m) {
+                const uint32_t u = unit + l * a.runs + m, buf = u % NU;
+                if (!open) {
+                  if (!W4T_WAIT(tempty0 + 8u * buf, ((u / NU) & 1u) ^ 1u)) break;
+                  tc_fence_after();
+                }
+                for (int k = 0; k < nmma; ++k) {
+                  const uint32_t off = (m * nmma + k) * 32;
+                  mma_i8_ss(tmem_base + buf * TN, smem_desc_sw128(ab + off, 16, 1024),
+                            smem_desc_sw128(xb + off, 16, 1024), IDESC, open || k != 0);
+                }
+                if (close) mma_commit(tfull0 + 8u * buf);
+              }
+              mma_commit(aempty0 + 8u * slot);
+              if (++slot == AS) { slot = 0; sph ^= 1u; }
+            }
+            mma_commit(empty0 + 8u * st);
+            if (++st == S) { st = 0; ph ^= 1u; }
+            open = !close;
+            if (close) unit += NL * a.runs;
+          }
+        }
+        if (!ok) {  // given up: the tensor cores are done before TMEM is freed
+          int own = 0;
+          mma_commit(drain);
+          mbar_wait_bounded(drain, 0, &own, a.wait_ns);
+        }
+      }
+    }
+  } else if (warp < UW) {
+    // -------------------------------------------------------------- unpack
+    W4T_FEWER();
+    const int r = threadIdx.x;  // row of the tile
+    const uint32_t in_row = r * 64, out_row = r * 128;
+    uint32_t st = 0, ph = 0, slot = 0, sph = 0;
+    for (int64_t t = tile0; t < tiles; t += tile_step) {
+      const int row = min(static_cast<int>(t / a.tok_tiles) * BM + r, p.d_row - 1);
+      const uint8_t* zr[NL];
+#pragma unroll
+      for (int l = 0; l < NL; ++l) zr[l] = p.layer[l].zeros + static_cast<size_t>(row) * p.n_groups;
+      uint32_t znext[NL];
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+        znext[l] = __ldg(zr[l] + min(c0 * CH / p.group, p.n_groups - 1));
+      for (int c = c0; c < c1; ++c) {
+        uint32_t z[NL][4];
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          if (a.runs == 1) {
+            z[l][0] = z[l][1] = z[l][2] = z[l][3] = znext[l] * 0x01010101u;
+            znext[l] = __ldg(zr[l] + min((c + 1) * CH / p.group, p.n_groups - 1));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              z[l][j] = __ldg(zr[l] + min((c * CH + 32 * j) / p.group, p.n_groups - 1)) * 0x01010101u;
+          }
+        }
+        W4T_WAIT(full0 + 8u * st, ph);
+        const uint8_t* in = base + st * C::STAGE_BYTES;
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          W4T_WAIT(aempty0 + 8u * slot, sph ^ 1u);
+          uint8_t* out = base + C::RING_BYTES + slot * SLOT_BYTES + out_row;
+          if (ok) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 w = *reinterpret_cast<const uint4*>(in + l * PACKED_BYTES + in_row +
+                                                              ((i ^ ((r >> 1) & 3)) << 4));
+              const uint2 b0 = unpack_word(w.x, z[l][i]), b1 = unpack_word(w.y, z[l][i]);
+              const uint2 b2 = unpack_word(w.z, z[l][i]), b3 = unpack_word(w.w, z[l][i]);
+              *reinterpret_cast<uint4*>(out + (((2 * i) ^ (r & 7)) << 4)) =
+                  make_uint4(b0.x, b0.y, b1.x, b1.y);
+              *reinterpret_cast<uint4*>(out + (((2 * i + 1) ^ (r & 7)) << 4)) =
+                  make_uint4(b2.x, b2.y, b3.x, b3.y);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(afull0 + 8u * slot);
+          if (++slot == AS) { slot = 0; sph ^= 1u; }
+        }
+        if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
+        if (++st == S) { st = 0; ph ^= 1u; }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    W4T_MORE();
+    const int e = threadIdx.x - UW * 32;
+    const int quarter = warp & 3, half = (warp - UW) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    constexpr int COLS = C::COLS;
+    uint32_t unit = 0, flip = 0;
+    for (int64_t t = tile0; t < tiles; t += tile_step) {
+      const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
+      const int64_t tok0 = (t % a.tok_tiles) * TN;
+      const int row = row0 + quarter * 32 + lane;
+      uint64_t acc[NL][COLS / 2];
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j) acc[l][j] = 0ull;
+      const float* sr[NL];
+#pragma unroll
+      for (int l = 0; l < NL; ++l)
+        sr[l] = p.layer[l].scales + static_cast<size_t>(min(row, p.d_row - 1)) * p.n_groups;
+      const float* xs = p.xs + min(tok0 + e, p.n - 1) * p.xgroups;
+      const bool per_token = p.xgroups == 1;
+      float snext[NL], xnext = 0.0f;
+#pragma unroll
+      for (int l = 0; l < NL; ++l) snext[l] = __ldg(sr[l] + min(c0 * CH / p.group, p.n_groups - 1));
+      if (e < TN) xnext = __ldg(xs + (per_token ? 0 : c0));
+      for (int c = c0; c < c1; ++c) {
+        if (!per_token || c == c0) {
+          // the tokens' scales of this chunk; two buffers, so one barrier a
+          // chunk keeps readers and the next writers apart
+          if (e < TN) {
+            sx[flip * TN + e] = xnext;
+            if (!per_token && c + 1 < c1) xnext = __ldg(xs + c + 1);
+          }
+          named_bar(1, EW * 32);
+          flip ^= 1u;
+        }
+        const float* sxc = sx + (flip ^ 1u) * TN + half * COLS;
+        if (!closes(c)) continue;
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          for (int m = 0; m < a.runs; ++m, ++unit) {
+            float sw;
+            if (a.runs == 1) {
+              sw = snext[l];
+              snext[l] = __ldg(sr[l] + min((c + 1) * CH / p.group, p.n_groups - 1));
+            } else {
+              sw = __ldg(sr[l] + min((c * CH + m * (CH / a.runs)) / p.group, p.n_groups - 1));
+            }
+            const uint32_t buf = unit % NU;
+            W4T_WAIT(tfull0 + 8u * buf, (unit / NU) & 1u);
+            ok = __all_sync(0xffffffffu, ok);  // the loads below are the whole warp's
+            if (ok) {
+              tc_fence_after();
+              const uint32_t t0 = tmem_base + lanes + buf * TN + half * COLS;
+              const uint64_t sw2 = pack2(sw, sw);
+#pragma unroll
+              for (int b = 0; b < COLS / 16; ++b) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(t0 + b * 16, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint64_t f0 = pack2(__int2float_rn(v[4 * q]), __int2float_rn(v[4 * q + 1]));
+                  const uint64_t f1 =
+                      pack2(__int2float_rn(v[4 * q + 2]), __int2float_rn(v[4 * q + 3]));
+                  uint64_t& a0 = acc[l][8 * b + 2 * q];
+                  uint64_t& a1 = acc[l][8 * b + 2 * q + 1];
+                  if (per_token) {
+                    a0 = fma2(f0, sw2, a0);
+                    a1 = fma2(f1, sw2, a1);
+                  } else {
+                    const float4 s = *reinterpret_cast<const float4*>(sxc + 16 * b + 4 * q);
+                    a0 = fma2(f0, mul2(sw2, pack2(s.x, s.y)), a0);
+                    a1 = fma2(f1, mul2(sw2, pack2(s.z, s.w)), a1);
+                  }
+                }
+              }
+              tc_fence_before();
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
+          }
+        }
+      }
+      if (per_token) {  // the token's only scale, once
+        const float* s = sx + (flip ^ 1u) * TN + half * COLS;
+#pragma unroll
+        for (int l = 0; l < NL; ++l)
+#pragma unroll
+          for (int j = 0; j < COLS / 2; ++j)
+            acc[l][j] = mul2(acc[l][j], *reinterpret_cast<const uint64_t*>(s + 2 * j));
+      }
+      if constexpr (C::BIG) {
+        const bool live = row < p.d_row;
+        const int64_t t1 = tok0 + half * COLS;
+        const int left = static_cast<int>(min(static_cast<int64_t>(COLS), p.n - t1));
+        const int64_t at = t1 * p.ldy + row;
+        if (NL == 2) {
+#pragma unroll
+          for (int j = 0; j < COLS / 2; ++j) {
+            const float2 g = unpack2(acc[0][j]), u = unpack2(acc[NL - 1][j]);
+            acc[0][j] = pack2(w4a8::silu_times(g.x, u.x), w4a8::silu_times(g.y, u.y));
+          }
+        }
+        if (NL == 2 && p.out == w4a8::OUT_I8) {
+          // maxima over the tile's 128 rows, through shared memory
+#pragma unroll
+          for (int j = 0; j < COLS / 2; ++j) {
+            const float2 h = unpack2(acc[0][j]);
+            const uint32_t m0 = __reduce_max_sync(0xffffffffu, live ? act8::abs_bits(h.x) : 0u);
+            const uint32_t m1 = __reduce_max_sync(0xffffffffu, live ? act8::abs_bits(h.y) : 0u);
+            if (lane == 0) {
+              tops[quarter * TN + half * COLS + 2 * j] = m0;
+              tops[quarter * TN + half * COLS + 2 * j + 1] = m1;
+            }
+          }
+          named_bar(1, EW * 32);
+          if (e < TN) {  // a thread a token: its scale, and what the rows multiply by
+            const act8::Quant q = act8::quant_of(
+                max(max(tops[e], tops[TN + e]), max(tops[2 * TN + e], tops[3 * TN + e])));
+            tops[e] = __float_as_uint(q.inv);
+            tops[TN + e] = __float_as_uint(q.lift);
+            if (tok0 + e < p.n) p.ys[(tok0 + e) * ((p.d_row + 127) / 128) + row0 / BM] = q.scale;
+          }
+          named_bar(1, EW * 32);
+          int8_t* y = static_cast<int8_t*>(p.y) + at;
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) {
+            act8::Quant q;
+            q.inv = __uint_as_float(tops[half * COLS + j]);
+            q.lift = __uint_as_float(tops[TN + half * COLS + j]);
+            const float2 h = unpack2(acc[0][j / 2]);
+            if (j < left && live)
+              y[j * p.ldy] = static_cast<int8_t>(act8::code_or_zero(j & 1 ? h.y : h.x, q));
+          }
+        } else if (live) {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) {
+            const float2 h = unpack2(acc[0][j / 2]);
+            if (j < left) w4a8::store_out(p, at + j * p.ldy, j & 1 ? h.y : h.x);
+          }
+        }
+        named_bar(1, EW * 32);  // the token scales are read before the next tile's
+      } else {
+        // the sums, token-major, over the ring: every copy has been consumed
+        named_bar(1, EW * 32);
+        float* sums = reinterpret_cast<float*>(base);
+#pragma unroll
+        for (int l = 0; l < NL; ++l)
+#pragma unroll
+          for (int j = 0; j < COLS / 2; ++j) {
+            const float2 v = unpack2(acc[l][j]);
+            float* to = sums + (l * TN + half * COLS + 2 * j) * BM + quarter * 32 + lane;
+            to[0] = v.x;
+            to[BM] = v.y;
+          }
+      }
+    }
+  }
+#undef W4T_WAIT
+#undef W4T_FEWER
+#undef W4T_MORE
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == UW + EW + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+  if constexpr (!C::BIG) {
+    // The cluster's CTAs each finish a share of the tokens, a warp a token and
+    // a lane four rows.  TMEM is free by now: no CTA holds it while it waits.
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    const int row0 = static_cast<int>(tile0 / a.tok_tiles) * BM;
+    const int64_t tok0 = (tile0 % a.tok_tiles) * TN;
+    const int ntok = static_cast<int>(min(static_cast<int64_t>(TN), p.n - tok0));
+    float* sums = reinterpret_cast<float*>(base);
+    for (int tk = krank + warp * a.ksplit; tk < ntok; tk += C::WARPS * a.ksplit) {
+      float4 v[NL];
+#pragma unroll
+      for (int l = 0; l < NL; ++l) {
+        float* own = sums + (l * TN + tk) * BM + 4 * lane;
+        v[l] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < a.ksplit; ++r) {
+          const float4 o = *reinterpret_cast<const float4*>(cl.map_shared_rank(own, r));
+          v[l].x += o.x; v[l].y += o.y; v[l].z += o.z; v[l].w += o.w;
+        }
+      }
+      float h[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+      if (NL == 2) {
+        h[0] = w4a8::silu_times(h[0], v[NL - 1].x);
+        h[1] = w4a8::silu_times(h[1], v[NL - 1].y);
+        h[2] = w4a8::silu_times(h[2], v[NL - 1].z);
+        h[3] = w4a8::silu_times(h[3], v[NL - 1].w);
+      }
+      const int row = row0 + 4 * lane;
+      const int64_t at = (tok0 + tk) * p.ldy + row;
+      if (NL == 2 && p.out == w4a8::OUT_I8) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < p.d_row) top = max(top, act8::abs_bits(h[i]));
+        const act8::Quant q = act8::quant_of(__reduce_max_sync(0xffffffffu, top));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < p.d_row)
+            static_cast<int8_t*>(p.y)[at + i] = static_cast<int8_t>(act8::code_or_zero(h[i], q));
+        if (lane == 0) p.ys[(tok0 + tk) * ((p.d_row + 127) / 128) + row0 / BM] = q.scale;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < p.d_row) w4a8::store_out(p, at + i, h[i]);
+      }
+    }
+    cl.sync();  // no CTA leaves while another may still read its sums
+  }
+}
+
+}  // namespace w4a8t
+}  // namespace gptq
