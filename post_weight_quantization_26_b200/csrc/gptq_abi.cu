@@ -91,10 +91,10 @@ struct DeviceInfo {
 template <bool GATED>
 struct W4a8Cfg {
   static constexpr int NL = GATED ? 2 : 1;
-  using Tiny = w4a8t::Cfg<NL, 16, 4, GATED ? 3 : 5, GATED ? 3 : 2, 2, false>;
-  using Small = w4a8t::Cfg<NL, 64 / NL, 4, GATED ? 3 : 4, GATED ? 3 : 2, 2, false>;
-  using Mid = w4a8t::Cfg<NL, 128 / NL, 8, 5, GATED ? 4 : 3, 1, false>;
-  using Big = w4a8t::Cfg<NL, 256 / NL, 8, 4, GATED ? 4 : 3, 1, true>;
+  using Tiny = w4a8t::Cfg<NL, 16, 4, 4, GATED ? 3 : 5, GATED ? 3 : 2, 2, false>;
+  using Small = w4a8t::Cfg<NL, 64 / NL, 4, GATED ? 4 : 8, GATED ? 3 : 4, 2, 2, false>;
+  using Mid = w4a8t::Cfg<NL, 128 / NL, 4, 8, 5, GATED ? 4 : 3, 1, false>;
+  using Big = w4a8t::Cfg<NL, 256 / NL, 8, 16, 4, GATED ? 4 : 3, 1, true>;
 };
 
 // The shared memory of a tile kernel, and the carveout that lets MINB CTAs of
@@ -595,6 +595,7 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   const int64_t tiles = w4a8_tiles<C>(p);
   const int nchunks = (p.d_col + w4a8t::CH - 1) / w4a8t::CH;
   a.runs = p.n_groups == 1 || p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
+  a.gmagic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.group - 1) / p.group);
   a.wait_ns = g_wait_ns.load();
   a.ksplit = 1;
   if (!C::BIG) {

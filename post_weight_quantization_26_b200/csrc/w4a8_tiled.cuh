@@ -44,31 +44,36 @@ constexpr int CH = 128;  // columns per chunk
 constexpr int PACKED_BYTES = BM * CH / 2;
 constexpr int SLOT_BYTES = BM * CH;
 
-// TN_: tokens per tile; EW_: epilogue warps; S_: ring stages; AS_: operand
-// slots of one layer and chunk; MINB: CTAs per SM.
-template <int NL_, int TN_, int EW_, int S_, int AS_, int MINB_, bool BIG_>
+// NL: layers; TN: tokens per tile; UW, EW: unpack and epilogue warps; S: ring
+// stages; AS: operand slots of one layer and chunk; MINB: CTAs per SM.  Four
+// more warps are the TMA warp, the MMA warp and two that fetch scales.
+template <int NL_, int TN_, int UW_, int EW_, int S_, int AS_, int MINB_, bool BIG_>
 struct Cfg {
-  static constexpr int NL = NL_, TN = TN_, EW = EW_, S = S_, AS = AS_, MINB = MINB_;
+  static constexpr int NL = NL_, TN = TN_, UW = UW_, EW = EW_, S = S_, AS = AS_, MINB = MINB_;
   static constexpr bool BIG = BIG_;
-  static constexpr int UW = 4;                       // unpack warps
-  static constexpr int WARPS = BIG ? 16 : UW + EW + 2;  // BIG: whole warpgroups
+  static constexpr int WARPS = UW + EW + 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int NU = 512 / MINB / TN < 4 ? 512 / MINB / TN : 4;  // TMEM buffers
-  static constexpr int TMEM_COLS = NU * TN;
+  static constexpr int TMEM_COLS = NU * TN < 32 ? 32 : NU * TN;
   static constexpr int COLS = TN / (EW / 4);         // columns (tokens) per epilogue warp
   static constexpr int X_BYTES = TN * CH;
   static constexpr int STAGE_BYTES = NL * PACKED_BYTES + X_BYTES;
   static constexpr int RING_BYTES = S * STAGE_BYTES;
   static constexpr int SUM_BYTES = BIG ? 0 : NL * TN * BM * 4;  // over the ring, at the end
-  static constexpr int SX_BYTES = 2 * TN * 4;
+  static constexpr int SX_BYTES = 2 * 4 * TN * 4;       // two sets of token scales
+  static constexpr int SW_BYTES = 2 * 4 * NL * BM * 4;  // two sets of row scales
   static constexpr int TOP_BYTES = BIG ? 4 * TN * 4 : 0;
-  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 1;
-  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + TOP_BYTES + BARS * 8 + 16 +
-                              1024 /* alignment */;
-  static_assert(NU >= NL && TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
+  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 5;
+  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + TOP_BYTES +
+                              BARS * 8 + 16 + 1024 /* alignment */;
+  static_assert(NU >= NL && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
-  static_assert(EW * 32 >= TN && COLS % 16 == 0, "epilogue threads");
-  static_assert(!BIG || TN * NL == 256, "registers");
+  static_assert(EW % 4 == 0 && UW % 4 == 0 && COLS % 16 == 0, "warps");
+  static_assert((SMEM + 1024) * MINB <= 228 * 1024, "shared memory");
+  // BIG moves registers between warpgroups: the launch's are THREADS x LAUNCH
+  static constexpr int LAUNCH = 65536 / THREADS / 8 * 8, MORE = 96,
+                       FEWER = (THREADS * LAUNCH - EW * 32 * MORE) / ((UW + 4) * 32) / 8 * 8;
+  static_assert(!BIG || (EW * MORE + (UW + 4) * FEWER) * 32 <= THREADS * LAUNCH, "registers");
 };
 
 struct Tiled {
@@ -76,6 +81,7 @@ struct Tiled {
   int row_tiles, tok_tiles;
   int ksplit;        // CTAs of a cluster along the columns
   int runs;          // runs per chunk: 4 (32 columns), 2, or 1
+  uint32_t gmagic;   // ceil(2^32 / group): umulhi(k, gmagic) == k / group for k, group <= 2^16
   uint64_t wait_ns;
 };
 
@@ -87,6 +93,14 @@ __device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // Four signed bytes q - z of one word's even or odd codes, still biased by 128.
@@ -122,6 +136,29 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// One run's sums of COLS tokens from TMEM, scaled and added to acc.  The
+// conversion to fp32 is an instruction of half the adders' rate; the add of
+// 1.5 * 2^23 and its subtraction would cost as much and more issue slots.
+template <int COLS>
+__device__ __forceinline__ void fold_run(uint64_t (&acc)[COLS / 2], uint32_t t0, float sw,
+                                         const float* sx) {
+  const uint64_t sw2 = pack2(sw, sw);
+#pragma unroll
+  for (int b = 0; b < COLS / 16; ++b) {
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(t0 + 16 * b, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 s = *reinterpret_cast<const float4*>(sx + 16 * b + 4 * q);
+      const uint64_t f0 = pack2(__int2float_rn(v[4 * q]), __int2float_rn(v[4 * q + 1]));
+      const uint64_t f1 = pack2(__int2float_rn(v[4 * q + 2]), __int2float_rn(v[4 * q + 3]));
+      acc[8 * b + 2 * q] = fma2(f0, mul2(sw2, pack2(s.x, s.y)), acc[8 * b + 2 * q]);
+      acc[8 * b + 2 * q + 1] = fma2(f1, mul2(sw2, pack2(s.z, s.w)), acc[8 * b + 2 * q + 1]);
+    }
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::MINB)
 w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
@@ -138,15 +175,18 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   uint8_t* base = smem_raw + (ring - raw);
   const uint32_t slots = ring + C::RING_BYTES;
   float* sx = reinterpret_cast<float*>(base + C::RING_BYTES + AS * SLOT_BYTES);
-  uint32_t* tops = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(sx) + C::SX_BYTES);
+  float* swb = sx + C::SX_BYTES / 4;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(swb + C::SW_BYTES / 4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, afull0 = empty0 + 8u * S,
                  aempty0 = afull0 + 8u * AS, tfull0 = aempty0 + 8u * AS,
-                 tempty0 = tfull0 + 8u * NU, drain = tempty0 + 8u * NU;
+                 tempty0 = tfull0 + 8u * NU, sfull0 = tempty0 + 8u * NU, sempty0 = sfull0 + 16u,
+                 drain = sempty0 + 16u;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const bool leader = elect_one();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, 1);
@@ -159,6 +199,10 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     for (int u = 0; u < NU; ++u) {
       mbar_init(tfull0 + 8u * u, 1);
       mbar_init(tempty0 + 8u * u, EW);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(sfull0 + 8u * u, 2);
+      mbar_init(sempty0 + 8u * u, EW);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -184,96 +228,168 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   const int64_t tile0 = C::BIG ? blockIdx.x : blockIdx.x / a.ksplit;
   const int64_t tile_step = C::BIG ? gridDim.x : tiles;
   // a chunk's last run closes its TMEM buffer unless neither scale changes
+  const bool every = p.xgroups != 1 || a.runs != 1 || p.group == CH;
+  auto group_of = [&](int col) {
+    return min(static_cast<int>(__umulhi(static_cast<uint32_t>(col), a.gmagic)), p.n_groups - 1);
+  };
   auto closes = [&](int c) {
-    return c == c1 - 1 || p.xgroups != 1 || a.runs != 1 ||
-           (p.n_groups != 1 && ((c + 1) * CH) % p.group == 0);
+    return every || c == c1 - 1 || group_of((c + 1) * CH) != group_of(c * CH);
   };
   bool ok = true;
 #define W4T_WAIT(bar, par) \
   (ok = ok && mbar_wait_bounded((bar), (par), abort_flag, a.wait_ns))
 
-  // BIG: 65536 registers at launch, 512 x 128 = 256 x 200 (epilogue) + 256 x 56
 #define W4T_FEWER() \
-  if (C::BIG) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;")
+  if (C::BIG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEWER))
 #define W4T_MORE() \
-  if (C::BIG) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;")
+  if (C::BIG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE))
 
   if (warp >= UW + EW) {
     W4T_FEWER();  // the whole warpgroup, at one place
     if (warp == UW + EW) {
       // ------------------------------------------------------------ TMA warp
-      if (lane == 0) {
-        uint32_t st = 0, ph = 0, issued = 0;
-        for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
-          const int row = static_cast<int>(t / a.tok_tiles) * BM;
-          const int tok = static_cast<int>(t % a.tok_tiles) * TN;
-          for (int c = c0; c < c1; ++c) {
-            if (!W4T_WAIT(empty0 + 8u * st, ph ^ 1u)) break;
-            const uint32_t fb = full0 + 8u * st, at = ring + st * C::STAGE_BYTES;
+      // The warp stays together and one thread issues, here and below.
+      uint32_t st = 0, ph = 0, issued = 0;
+      for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
+        const int row = static_cast<int>(t / a.tok_tiles) * BM;
+        const int tok = static_cast<int>(t % a.tok_tiles) * TN;
+        for (int c = c0; c < c1; ++c) {
+          if (!W4T_WAIT(empty0 + 8u * st, ph ^ 1u)) break;
+          const uint32_t fb = full0 + 8u * st, at = ring + st * C::STAGE_BYTES;
+          if (leader) {
             mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
             tma_load_2d(at, &tmap_w0, fb, c * (CH / 2), row);
             if (NL == 2) tma_load_2d(at + PACKED_BYTES, &tmap_w1, fb, c * (CH / 2), row);
             tma_load_2d(at + NL * PACKED_BYTES, &tmap_x, fb, c * CH, tok);
             ++issued;
-            if (++st == S) { st = 0; ph ^= 1u; }
           }
+          __syncwarp();
+          if (++st == S) { st = 0; ph ^= 1u; }
         }
-        if (!ok) {  // given up: no copy may land in memory that is handed on
-          int own = 0;
-          for (uint32_t k = 0; k < S && k < issued; ++k) {
-            const uint32_t i = issued - 1 - k;
-            mbar_wait_bounded(full0 + 8u * (i % S), (i / S) & 1u, &own, a.wait_ns);
-          }
+      }
+      if (!ok && leader) {  // given up: no copy may land in memory that is handed on
+        int own = 0;
+        for (uint32_t k = 0; k < S && k < issued; ++k) {
+          const uint32_t i = issued - 1 - k;
+          mbar_wait_bounded(full0 + 8u * (i % S), (i / S) & 1u, &own, a.wait_ns);
         }
       }
     } else if (warp == UW + EW + 1) {
       // ------------------------------------------------------------ MMA warp
-      if (lane == 0) {
-        uint32_t st = 0, ph = 0, slot = 0, sph = 0, unit = 0;
-        bool open = false;  // the current buffers hold a started run
-        for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
-          for (int c = c0; c < c1 && ok; ++c) {
-            if (!W4T_WAIT(full0 + 8u * st, ph)) break;
-            const uint32_t xb = ring + st * C::STAGE_BYTES + NL * PACKED_BYTES;
-            const bool close = closes(c);
-            const int nmma = 4 / a.runs;
-            for (int l = 0; l < NL && ok; ++l) {
-              if (!W4T_WAIT(afull0 + 8u * slot, sph)) break;
+      const uint64_t DESC = smem_desc_sw128(0, 16, 1024);  // addresses are added
+      uint32_t st = 0, ph = 0, slot = 0, sph = 0, unit = 0;
+      bool open = false;  // the current buffers hold a started run
+      for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
+        for (int c = c0; c < c1 && ok; ++c) {
+          const bool close = closes(c);
+          if (!W4T_WAIT(full0 + 8u * st, ph)) break;
+          const uint64_t xd = DESC + ((ring + st * C::STAGE_BYTES + NL * PACKED_BYTES) >> 4);
+#pragma unroll
+          for (int l = 0; l < NL; ++l) {
+            const uint64_t ad = DESC + ((slots + slot * SLOT_BYTES) >> 4);
+            W4T_WAIT(afull0 + 8u * slot, sph);
+            // 32 columns are 32 bytes: 2 units of a descriptor's address
+            if (a.runs == 1) {
+              const uint32_t u = unit + l, buf = u % NU, d = tmem_base + buf * TN;
+              if (!open) W4T_WAIT(tempty0 + 8u * buf, ((u / NU) & 1u) ^ 1u);
               tc_fence_after();
-              const uint32_t ab = slots + slot * SLOT_BYTES;
-              for (int m = 0; m < a.runs; ++m) {
-                const uint32_t u = unit + l * a.runs + m, buf = u % NU;
-                if (!open) {
-                  if (!W4T_WAIT(tempty0 + 8u * buf, ((u / NU) & 1u) ^ 1u)) break;
-                  tc_fence_after();
-                }
-                for (int k = 0; k < nmma; ++k) {
-                  const uint32_t off = (m * nmma + k) * 32;
-                  mma_i8_ss(tmem_base + buf * TN, smem_desc_sw128(ab + off, 16, 1024),
-                            smem_desc_sw128(xb + off, 16, 1024), IDESC, open || k != 0);
-                }
+              if (ok && leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_i8_ss(d, ad + 2 * k, xd + 2 * k, IDESC, k != 0 || open);
                 if (close) mma_commit(tfull0 + 8u * buf);
               }
-              mma_commit(aempty0 + 8u * slot);
-              if (++slot == AS) { slot = 0; sph ^= 1u; }
+            } else {
+              for (int m = 0; m < a.runs; ++m) {
+                const uint32_t u = unit + l * a.runs + m, buf = u % NU, d = tmem_base + buf * TN;
+                W4T_WAIT(tempty0 + 8u * buf, ((u / NU) & 1u) ^ 1u);
+                tc_fence_after();
+                if (ok && leader) {
+                  if (a.runs == 2) {
+                    mma_i8_ss(d, ad + 4 * m, xd + 4 * m, IDESC, 0);
+                    mma_i8_ss(d, ad + 4 * m + 2, xd + 4 * m + 2, IDESC, 1);
+                  } else {
+                    mma_i8_ss(d, ad + 2 * m, xd + 2 * m, IDESC, 0);
+                  }
+                  mma_commit(tfull0 + 8u * buf);
+                }
+              }
             }
-            mma_commit(empty0 + 8u * st);
-            if (++st == S) { st = 0; ph ^= 1u; }
-            open = !close;
-            if (close) unit += NL * a.runs;
+            if (ok && leader) mma_commit(aempty0 + 8u * slot);
+            if (++slot == AS) { slot = 0; sph ^= 1u; }
           }
+          if (ok && leader) mma_commit(empty0 + 8u * st);
+          __syncwarp();
+          if (++st == S) { st = 0; ph ^= 1u; }
+          open = !close;
+          if (close) unit += NL * a.runs;
         }
-        if (!ok) {  // given up: the tensor cores are done before TMEM is freed
-          int own = 0;
-          mma_commit(drain);
-          mbar_wait_bounded(drain, 0, &own, a.wait_ns);
+      }
+      if (!ok && leader) {  // given up: the tensor cores are done before TMEM is freed
+        int own = 0;
+        mma_commit(drain);
+        mbar_wait_bounded(drain, 0, &own, a.wait_ns);
+      }
+    } else {
+      // --------------------------------------------------------- scale warps
+      // The scales of the next runs, in sets of four runs (4, 2 or 1 chunks):
+      // their row scales, and their chunks' token scales.
+      const int i = threadIdx.x - (UW + EW + 2) * 32;  // 0..63
+      const int per_set = 4 / a.runs, step = CH / a.runs;
+      uint32_t set = 0;
+      for (int64_t t = tile0; t < tiles; t += tile_step) {
+        const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
+        const int64_t tok0 = (t % a.tok_tiles) * TN;
+        for (int cs = c0; cs < c1; cs += per_set, ++set) {
+          int gi[4], ci[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            gi[j] = group_of(cs * CH + j * step);
+            ci[j] = p.xgroups == 1 ? 0 : min(cs + j, nchunks - 1);
+          }
+          const uint32_t at = set & 1u;
+          W4T_WAIT(sempty0 + 8u * at, ((set >> 1) & 1u) ^ 1u);
+          float* xo = sx + at * 4 * TN;
+          float* wo = swb + at * NL * 4 * BM;
+#pragma unroll
+          for (int l = 0; l < NL; ++l) {
+            float v[BM / 64][4];
+#pragma unroll
+            for (int k = 0; k < BM / 64; ++k) {
+              const float* from = p.layer[l].scales +
+                                  static_cast<size_t>(min(row0 + i + 64 * k, p.d_row - 1)) * p.n_groups;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[k][j] = __ldg(from + gi[j]);
+            }
+#pragma unroll
+            for (int k = 0; k < BM / 64; ++k)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) wo[(l * 4 + j) * BM + i + 64 * k] = v[k][j];
+          }
+          constexpr int TK = (TN + 63) / 64;  // tokens of a thread
+          float v[TK][4];
+#pragma unroll
+          for (int k = 0; k < TK; ++k) {
+            const float* from = p.xs + min(tok0 + i + 64 * k, p.n - 1) * p.xgroups;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[k][j] = __ldg(from + ci[j]);
+          }
+#pragma unroll
+          for (int k = 0; k < TK; ++k)
+            if (TN % 64 == 0 || i + 64 * k < TN)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) xo[j * TN + i + 64 * k] = v[k][j];
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(sfull0 + 8u * at);
         }
       }
     }
   } else if (warp < UW) {
     // -------------------------------------------------------------- unpack
     W4T_FEWER();
-    const int r = threadIdx.x;  // row of the tile
+    const int r = threadIdx.x & (BM - 1);  // row of the tile
+    constexpr int PIECES = 16 / UW;        // 16-byte pieces (32 codes) of a thread
+    const int i0 = (threadIdx.x / BM) * PIECES;
     const uint32_t in_row = r * 64, out_row = r * 128;
     uint32_t st = 0, ph = 0, slot = 0, sph = 0;
     for (int64_t t = tile0; t < tiles; t += tile_step) {
@@ -281,49 +397,59 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       const uint8_t* zr[NL];
 #pragma unroll
       for (int l = 0; l < NL; ++l) zr[l] = p.layer[l].zeros + static_cast<size_t>(row) * p.n_groups;
-      uint32_t znext[NL];
+      // Zero points come four at a time, one set ahead: of four chunks, or of
+      // one chunk's runs of 32 columns where a run may end inside it.
+      const bool fine = a.runs != 1;
+      const int per_set = fine ? 1 : 4, zstep = fine ? 32 : CH;
+      uint32_t znext[NL][4];
+      auto load_z = [&](int c) {
 #pragma unroll
-      for (int l = 0; l < NL; ++l)
-        znext[l] = __ldg(zr[l] + min(c0 * CH / p.group, p.n_groups - 1));
-      for (int c = c0; c < c1; ++c) {
-        uint32_t z[NL][4];
+        for (int l = 0; l < NL; ++l)
 #pragma unroll
-        for (int l = 0; l < NL; ++l) {
-          if (a.runs == 1) {
-            z[l][0] = z[l][1] = z[l][2] = z[l][3] = znext[l] * 0x01010101u;
-            znext[l] = __ldg(zr[l] + min((c + 1) * CH / p.group, p.n_groups - 1));
-          } else {
+          for (int j = 0; j < 4; ++j) znext[l][j] = __ldg(zr[l] + group_of(c * CH + j * zstep));
+      };
+      load_z(c0);
+      for (int cs = c0; cs < c1; cs += per_set) {
+        uint32_t z[NL];  // a byte each
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              z[l][j] = __ldg(zr[l] + min((c * CH + 32 * j) / p.group, p.n_groups - 1)) * 0x01010101u;
-          }
-        }
-        W4T_WAIT(full0 + 8u * st, ph);
-        const uint8_t* in = base + st * C::STAGE_BYTES;
+        for (int l = 0; l < NL; ++l)
+          z[l] = znext[l][0] | (znext[l][1] << 8) | (znext[l][2] << 16) | (znext[l][3] << 24);
+        load_z(cs + per_set);
+        const int ce = min(cs + per_set, c1);
+#pragma unroll 1
+        for (int c = cs; c < ce; ++c) {
+          W4T_WAIT(full0 + 8u * st, ph);
+          const uint8_t* in = base + st * C::STAGE_BYTES + in_row;
 #pragma unroll
-        for (int l = 0; l < NL; ++l) {
-          W4T_WAIT(aempty0 + 8u * slot, sph ^ 1u);
-          uint8_t* out = base + C::RING_BYTES + slot * SLOT_BYTES + out_row;
-          if (ok) {
+          for (int l = 0; l < NL; ++l) {
+            const uint32_t zc = __byte_perm(z[l], 0, (c - cs) * 0x1111);  // a chunk's only one
+            uint4 w[PIECES];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 w = *reinterpret_cast<const uint4*>(in + l * PACKED_BYTES + in_row +
-                                                              ((i ^ ((r >> 1) & 3)) << 4));
-              const uint2 b0 = unpack_word(w.x, z[l][i]), b1 = unpack_word(w.y, z[l][i]);
-              const uint2 b2 = unpack_word(w.z, z[l][i]), b3 = unpack_word(w.w, z[l][i]);
-              *reinterpret_cast<uint4*>(out + (((2 * i) ^ (r & 7)) << 4)) =
-                  make_uint4(b0.x, b0.y, b1.x, b1.y);
-              *reinterpret_cast<uint4*>(out + (((2 * i + 1) ^ (r & 7)) << 4)) =
-                  make_uint4(b2.x, b2.y, b3.x, b3.y);
+            for (int i = 0; i < PIECES; ++i)
+              w[i] = *reinterpret_cast<const uint4*>(in + l * PACKED_BYTES +
+                                                     (((i0 + i) ^ ((r >> 1) & 3)) << 4));
+            W4T_WAIT(aempty0 + 8u * slot, sph ^ 1u);
+            uint8_t* out = base + C::RING_BYTES + slot * SLOT_BYTES + out_row;
+            if (ok) {
+#pragma unroll
+              for (int i = 0; i < PIECES; ++i) {
+                const uint32_t zi = fine ? __byte_perm(z[l], 0, (i0 + i) * 0x1111) : zc;
+                const uint2 b0 = unpack_word(w[i].x, zi), b1 = unpack_word(w[i].y, zi);
+                const uint2 b2 = unpack_word(w[i].z, zi), b3 = unpack_word(w[i].w, zi);
+                *reinterpret_cast<uint4*>(out + (((2 * (i0 + i)) ^ (r & 7)) << 4)) =
+                    make_uint4(b0.x, b0.y, b1.x, b1.y);
+                *reinterpret_cast<uint4*>(out + (((2 * (i0 + i) + 1) ^ (r & 7)) << 4)) =
+                    make_uint4(b2.x, b2.y, b3.x, b3.y);
+              }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(afull0 + 8u * slot);
+            if (++slot == AS) { slot = 0; sph ^= 1u; }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (ok && lane == 0) mbar_arrive(afull0 + 8u * slot);
-          if (++slot == AS) { slot = 0; sph ^= 1u; }
+          if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
+          if (++st == S) { st = 0; ph ^= 1u; }
         }
-        if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
-        if (++st == S) { st = 0; ph ^= 1u; }
       }
     }
   } else {
@@ -333,7 +459,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     const int quarter = warp & 3, half = (warp - UW) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     constexpr int COLS = C::COLS;
-    uint32_t unit = 0, flip = 0;
+    const int per_set = 4 / a.runs;
+    uint32_t unit = 0, set = 0;
     for (int64_t t = tile0; t < tiles; t += tile_step) {
       const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
       const int64_t tok0 = (t % a.tok_tiles) * TN;
@@ -343,82 +470,36 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       for (int l = 0; l < NL; ++l)
 #pragma unroll
         for (int j = 0; j < COLS / 2; ++j) acc[l][j] = 0ull;
-      const float* sr[NL];
+      for (int cs = c0; cs < c1; cs += per_set, ++set) {
+        const uint32_t at = set & 1u;
+        W4T_WAIT(sfull0 + 8u * at, (set >> 1) & 1u);
+        const float* sxs = sx + at * 4 * TN + half * COLS;
+        const float* sws = swb + at * NL * 4 * BM + quarter * 32 + lane;
+        const int ce = min(cs + per_set, c1);
+#pragma unroll 1
+        for (int c = cs; c < ce; ++c, sxs += TN) {
+          if (!closes(c)) continue;
+#pragma unroll 1
+          for (int m = 0; m < a.runs; ++m) {
 #pragma unroll
-      for (int l = 0; l < NL; ++l)
-        sr[l] = p.layer[l].scales + static_cast<size_t>(min(row, p.d_row - 1)) * p.n_groups;
-      const float* xs = p.xs + min(tok0 + e, p.n - 1) * p.xgroups;
-      const bool per_token = p.xgroups == 1;
-      float snext[NL], xnext = 0.0f;
-#pragma unroll
-      for (int l = 0; l < NL; ++l) snext[l] = __ldg(sr[l] + min(c0 * CH / p.group, p.n_groups - 1));
-      if (e < TN) xnext = __ldg(xs + (per_token ? 0 : c0));
-      for (int c = c0; c < c1; ++c) {
-        if (!per_token || c == c0) {
-          // the tokens' scales of this chunk; two buffers, so one barrier a
-          // chunk keeps readers and the next writers apart
-          if (e < TN) {
-            sx[flip * TN + e] = xnext;
-            if (!per_token && c + 1 < c1) xnext = __ldg(xs + c + 1);
-          }
-          named_bar(1, EW * 32);
-          flip ^= 1u;
-        }
-        const float* sxc = sx + (flip ^ 1u) * TN + half * COLS;
-        if (!closes(c)) continue;
-#pragma unroll
-        for (int l = 0; l < NL; ++l) {
-          for (int m = 0; m < a.runs; ++m, ++unit) {
-            float sw;
-            if (a.runs == 1) {
-              sw = snext[l];
-              snext[l] = __ldg(sr[l] + min((c + 1) * CH / p.group, p.n_groups - 1));
-            } else {
-              sw = __ldg(sr[l] + min((c * CH + m * (CH / a.runs)) / p.group, p.n_groups - 1));
-            }
-            const uint32_t buf = unit % NU;
-            W4T_WAIT(tfull0 + 8u * buf, (unit / NU) & 1u);
-            ok = __all_sync(0xffffffffu, ok);  // the loads below are the whole warp's
-            if (ok) {
-              tc_fence_after();
-              const uint32_t t0 = tmem_base + lanes + buf * TN + half * COLS;
-              const uint64_t sw2 = pack2(sw, sw);
-#pragma unroll
-              for (int b = 0; b < COLS / 16; ++b) {
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(t0 + b * 16, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint64_t f0 = pack2(__int2float_rn(v[4 * q]), __int2float_rn(v[4 * q + 1]));
-                  const uint64_t f1 =
-                      pack2(__int2float_rn(v[4 * q + 2]), __int2float_rn(v[4 * q + 3]));
-                  uint64_t& a0 = acc[l][8 * b + 2 * q];
-                  uint64_t& a1 = acc[l][8 * b + 2 * q + 1];
-                  if (per_token) {
-                    a0 = fma2(f0, sw2, a0);
-                    a1 = fma2(f1, sw2, a1);
-                  } else {
-                    const float4 s = *reinterpret_cast<const float4*>(sxc + 16 * b + 4 * q);
-                    a0 = fma2(f0, mul2(sw2, pack2(s.x, s.y)), a0);
-                    a1 = fma2(f1, mul2(sw2, pack2(s.z, s.w)), a1);
-                  }
-                }
+            for (int l = 0; l < NL; ++l) {
+              const uint32_t u = unit + l * a.runs + m, buf = u % NU;
+              const float sw = sws[(l * 4 + (c - cs) * a.runs + m) * BM];
+              W4T_WAIT(tfull0 + 8u * buf, (u / NU) & 1u);
+              ok = __all_sync(0xffffffffu, ok);  // the loads below are the whole warp's
+              if (ok) {
+                tc_fence_after();
+                fold_run<COLS>(acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs);
+                tc_fence_before();
               }
-              tc_fence_before();
+              __syncwarp();
+              if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
             }
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
           }
+          unit += NL * a.runs;
         }
-      }
-      if (per_token) {  // the token's only scale, once
-        const float* s = sx + (flip ^ 1u) * TN + half * COLS;
-#pragma unroll
-        for (int l = 0; l < NL; ++l)
-#pragma unroll
-          for (int j = 0; j < COLS / 2; ++j)
-            acc[l][j] = mul2(acc[l][j], *reinterpret_cast<const uint64_t*>(s + 2 * j));
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(sempty0 + 8u * at);
       }
       if constexpr (C::BIG) {
         const bool live = row < p.d_row;
@@ -445,7 +526,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             }
           }
           named_bar(1, EW * 32);
-          if (e < TN) {  // a thread a token: its scale, and what the rows multiply by
+          if (e < TN) {  // one thread a token: its scale, and what the rows multiply by
             const act8::Quant q = act8::quant_of(
                 max(max(tops[e], tops[TN + e]), max(tops[2 * TN + e], tops[3 * TN + e])));
             tops[e] = __float_as_uint(q.inv);
@@ -463,6 +544,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (j < left && live)
               y[j * p.ldy] = static_cast<int8_t>(act8::code_or_zero(j & 1 ? h.y : h.x, q));
           }
+          named_bar(1, EW * 32);  // all have read before the next tile's maxima
         } else if (live) {
 #pragma unroll
           for (int j = 0; j < COLS; ++j) {
@@ -470,7 +552,6 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (j < left) w4a8::store_out(p, at + j * p.ldy, j & 1 ? h.y : h.x);
           }
         }
-        named_bar(1, EW * 32);  // the token scales are read before the next tile's
       } else {
         // the sums, token-major, over the ring: every copy has been consumed
         named_bar(1, EW * 32);

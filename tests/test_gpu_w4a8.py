@@ -201,6 +201,37 @@ def test_same_layer_twice_and_repeats(G, n):
         assert all(torch.equal(a, b) for a, b in zip(got, both(held)))
 
 
+# enough tiles for the persistent kernel (more than one a CTA), odd in every way
+@pytest.mark.parametrize("shape", [(130, 160, 0, 40000), (300, 416, 32, 13001), (129, 640, 128, 39000),
+                                   (257, 384, 64, 19777), (200, 1024, 256, 25001), (64, 96, 96, 50000)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("xg", [0, 128])
+def test_many_tokens(G, shape, xg):
+    rows, cols, group, n = shape
+    kw = {"block": 32} if group and group % 64 else {}
+    gate, up = small(layer(rows, cols, group, 1)), small(layer(rows, cols, group, 2))
+    codes, scales = acts(n, cols, xg)
+    cfg = G.make_config(bits=4, group_size=group, **kw)
+    y = G.gptq_w4a8_matmul(*gate, cfg, codes, scales, dtype=F32)
+    h = G.gptq_w4a8_gated(gate, up, cfg, codes, scales, dtype=BF)
+    h8, hs = G.gptq_w4a8_gated(gate, up, cfg, codes, scales, dtype=I8)
+    assert G.gptq_device_status() == 0
+    # every token of some stretches: the first and last tiles and one between
+    tok = np.unique(np.concatenate([np.arange(260), np.arange(n // 2, n // 2 + 130),
+                                    np.arange(n - 300, n)]))
+    c, s = codes[tok].cpu().numpy(), scales[tok].cpu().numpy()
+    R.check_float(y[tok].cpu().numpy(), *R.product(*np_layer(gate), group, c, s))
+    ref, bound = R.gated(np_layer(gate), np_layer(up), group, c, s)
+    R.check_float(h[tok].double().cpu().numpy(), ref, bound, bf16=True)
+    R.check_codes(h8[tok].cpu().numpy(), hs[tok].cpu().numpy(), ref, bound, 128)
+    # and all tokens against the same tokens in small batches, within twice the bound
+    whole = y.double()
+    for a in range(0, n, 9973):
+        part = G.gptq_w4a8_matmul(*gate, cfg, codes[a:a + 100], scales[a:a + 100].contiguous())
+        top = float(part.abs().max())
+        assert float((whole[a:a + 100] - part).abs().max()) <= 1e-5 * top
+
+
 # layers of the 65B and 7B shapes on sampled rows
 @pytest.mark.parametrize("case", [(8192, 22016, 128, 1), (8192, 22016, 128, 16),
                                   (22016, 8192, 128, 4), (4096, 11008, 0, 33),
