@@ -100,6 +100,132 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf) {
   return __reduce_max_sync(0xffffffffu, lane < warps ? buf[lane] : 0u);
 }
 
+// Eight consecutive elements as fp32, 16 or 32 aligned bytes.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+// Round v to the type, store it, and leave the rounded values in v.
+__device__ __forceinline__ void store8(float* p, float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Codes of eight values as two words.
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], const Quant& q) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(fmaf(y[i] * q.lift, q.inv, 12582912.0f));
+  if (q.inv == 0.0f) return make_uint2(0u, 0u);
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
+
+// Aligned rows of whole vectors of eight: one block a token, NV vectors a
+// thread in registers, so the pass reads and writes each byte once and is
+// bound by HBM (16384 x 8192 bf16 with residual: 939 MB).  Sixteen lanes hold
+// a group of 128 columns.
+template <typename TX, typename TR, int NV>
+__global__ void __launch_bounds__(NV == 8 ? 512 : 1024 / NV) rmsnorm_quant8_kernel(const Params p) {
+  __shared__ float sums[32];
+  __shared__ uint32_t tops[32];
+  const int64_t t = blockIdx.x;
+  const int nvec = p.d >> 3;
+  const TX* x = static_cast<const TX*>(p.x) + t * p.ldx;
+  float v[NV][8], r[8];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = threadIdx.x + i * blockDim.x;
+    if (k < nvec) load8(x + 8 * k, v[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+  }
+  if (p.res) {
+    const TR* res = static_cast<const TR*>(p.res) + t * p.ldr;
+    TR* out = static_cast<TR*>(p.res_out) + t * p.ldo;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = threadIdx.x + i * blockDim.x;
+      if (k < nvec) {
+        load8(res + 8 * k, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+        store8(out + 8 * k, v[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += v[i][j] * v[i][j];
+  sum = block_sum(sum, sums);
+  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+  uint32_t top[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = threadIdx.x + i * blockDim.x;
+    if (p.weight && k < nvec) {
+      load8(p.weight + 8 * k, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * r[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
+    }
+    top[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top[i] = max(top[i], abs_bits(v[i][j]));
+    if (k >= nvec) top[i] = 0;  // 0 * infinity
+  }
+  int8_t* codes = p.codes + t * p.ldq;
+  if (p.n_groups == 1) {
+#pragma unroll
+    for (int i = 1; i < NV; ++i) top[0] = max(top[0], top[i]);
+    const Quant q = quant_of(block_max(top[0], tops));
+    if (threadIdx.x == 0) p.scales[t] = q.scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = threadIdx.x + i * blockDim.x;
+      if (k < nvec) *reinterpret_cast<uint2*>(codes + 8 * k) = codes8(v[i], q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = threadIdx.x + i * blockDim.x;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+      const Quant q = quant_of(top[i]);
+      if (k < nvec) {
+        *reinterpret_cast<uint2*>(codes + 8 * k) = codes8(v[i], q);
+        if ((k & 15) == 0) p.scales[t * p.n_groups + (k >> 4)] = q.scale;
+      }
+    }
+  }
+}
+
 // Any width, stride and alignment: one block a token, three passes that read
 // r back from where it is (the caches).  A warp owns whole groups of 128
 // columns, four a lane, and each element is only ever touched by one thread,

@@ -91,22 +91,33 @@ struct DeviceInfo {
 template <bool GATED>
 struct W4a8Cfg {
   static constexpr int NL = GATED ? 2 : 1;
-  using Tiny = w4a8t::Cfg<NL, 16, 4, 4, GATED ? 3 : 5, GATED ? 3 : 2, 2, false>;
   using Small = w4a8t::Cfg<NL, 64 / NL, 4, GATED ? 4 : 8, GATED ? 3 : 4, 2, 2, false>;
   using Mid = w4a8t::Cfg<NL, 128 / NL, 4, 8, 5, GATED ? 4 : 3, 1, false>;
   using Big = w4a8t::Cfg<NL, 256 / NL, 8, 16, 4, GATED ? 4 : 3, 1, true>;
 };
 
-// The shared memory of a tile kernel, and the carveout that lets MINB CTAs of
-// it share an SM.
-template <class C>
-cudaError_t w4a8_allow_smem() {
-  const auto f = w4a8t::w4a8_tiled_kernel<C>;
+// The shared memory of a kernel, and the carveout that lets several of its
+// CTAs share an SM.
+template <typename F>
+cudaError_t allow_smem(F* f, int bytes) {
   const cudaError_t e =
-      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                               cudaSharedmemCarveoutMaxShared);
+}
+template <class C>
+cudaError_t w4a8_allow_smem() {
+  return allow_smem(w4a8t::w4a8_tiled_kernel<C>, C::SMEM);
+}
+template <int NL, int NT>
+cudaError_t w4a8_allow_rows() {
+  cudaError_t e = allow_smem(w4a8::w4a8_rows_kernel<w4a8::Cfg<NL, 4, NT>>, w4a8::Cfg<NL, 4, NT>::SMEM);
+  if (e == cudaSuccess)
+    e = allow_smem(w4a8::w4a8_rows_kernel<w4a8::Cfg<NL, 2, NT>>, w4a8::Cfg<NL, 2, NT>::SMEM);
+  if (e == cudaSuccess)
+    e = allow_smem(w4a8::w4a8_rows_kernel<w4a8::Cfg<NL, 1, NT>>, w4a8::Cfg<NL, 1, NT>::SMEM);
+  return e;
 }
 
 std::mutex g_mu;
@@ -135,11 +146,13 @@ gptq_status device_setup(int* num_sms) {
                           reinterpret_cast<const void*>(w4a16::w4a16_matmul_kernel<1, 1>)})
       GPTQ_CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          w4a16::WARPS * w4a16::WARP_BUDGET + w4a16::RED_BYTES));
-    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Tiny>());
+    GPTQ_CUDA_TRY((w4a8_allow_rows<1, 1>()));
+    GPTQ_CUDA_TRY((w4a8_allow_rows<1, 2>()));
+    GPTQ_CUDA_TRY((w4a8_allow_rows<2, 1>()));
+    GPTQ_CUDA_TRY((w4a8_allow_rows<2, 2>()));
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Small>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Mid>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<false>::Big>());
-    GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Tiny>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Small>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Mid>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Big>());
@@ -483,6 +496,33 @@ gptq_status gptq_w4a16_matmul(const uint32_t* qweight, const float* scales,
   return GPTQ_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// NV vectors of eight a thread: one for few tokens, where only latency counts
+// and a row wants many threads; four for many, with more bytes in flight a
+// thread and two or more rows on an SM.
+template <typename TX, typename TR>
+void norm_launch(const act8::Params& p, bool fast, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(p.n);
+  const int nvec = p.d / 8;
+  auto threads = [&](int nv) { return static_cast<unsigned>(((nvec + nv - 1) / nv + 31) / 32 * 32); };
+  if (!fast) act8::rmsnorm_quant8_any_kernel<TX, TR><<<grid, 256, 0, s>>>(p);
+  else if (nvec <= 1024 && (p.n <= 148 || nvec <= 128))
+    act8::rmsnorm_quant8_kernel<TX, TR, 1><<<grid, threads(1), 0, s>>>(p);
+  else if (nvec <= 512)
+    act8::rmsnorm_quant8_kernel<TX, TR, 2><<<grid, threads(2), 0, s>>>(p);
+  else if (nvec <= 1024)
+    act8::rmsnorm_quant8_kernel<TX, TR, 4><<<grid, threads(4), 0, s>>>(p);
+  else
+    act8::rmsnorm_quant8_kernel<TX, TR, 8><<<grid, threads(8), 0, s>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
 gptq_status gptq_rmsnorm_quant8(const void* X, int x_type, int64_t ldx, const void* residual,
                                 int r_type, int64_t ldr, const float* weight, double eps,
                                 int64_t n, int64_t d, int group, void* residual_out, int64_t ldo,
@@ -516,12 +556,19 @@ gptq_status gptq_rmsnorm_quant8(const void* X, int x_type, int64_t ldx, const vo
   p.n_groups = group ? (p.d + act8::GROUP - 1) / act8::GROUP : 1;
   p.eps = eps_f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(n);
+  // Whole, aligned vectors of eight elements keep a row in registers; up to
+  // 32768 columns fit.
+  auto vectors = [](const void* q, int64_t ld, size_t bytes, size_t unit) {
+    return aligned(q, unit) && (ld * static_cast<int64_t>(bytes)) % static_cast<int64_t>(unit) == 0;
+  };
+  const bool fast = d % 8 == 0 && d <= 32768 && vectors(X, ldx, xb, 16) && vectors(codes, ldq, 1, 8) &&
+                    (!weight || aligned(weight, 16)) &&
+                    (!residual || (vectors(residual, ldr, rb, 16) && vectors(residual_out, ldo, rb, 16)));
   const bool xf = x_type == GPTQ_F32, rf = r_type == GPTQ_F32;
-  if (xf && rf) act8::rmsnorm_quant8_any_kernel<float, float><<<grid, 256, 0, s>>>(p);
-  else if (xf) act8::rmsnorm_quant8_any_kernel<float, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
-  else if (rf) act8::rmsnorm_quant8_any_kernel<__nv_bfloat16, float><<<grid, 256, 0, s>>>(p);
-  else act8::rmsnorm_quant8_any_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  if (xf && rf) norm_launch<float, float>(p, fast, s);
+  else if (xf) norm_launch<float, __nv_bfloat16>(p, fast, s);
+  else if (rf) norm_launch<__nv_bfloat16, float>(p, fast, s);
+  else norm_launch<__nv_bfloat16, __nv_bfloat16>(p, fast, s);
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
@@ -551,34 +598,83 @@ gptq_status encode_u8_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64
   return GPTQ_OK;
 }
 
-// Few tokens: one launch of the row kernel.
-template <bool GATED>
-gptq_status w4a8_rows(const w4a8::Params& p, cudaStream_t s) {
+// Few tokens (at most 8 NT): one launch of the row kernel.
+template <class C>
+gptq_status w4a8_rows_launch(const w4a8::Params& p, int num_sms, cudaStream_t s) {
+  w4a8::Launch a{};
+  a.p = p;
+  a.wait_ns = g_wait_ns.load();
+  a.whole = p.d_col % 128 == 0;
+  CUtensorMap mw[2], mx;
+  for (int l = 0; l < 2; ++l) {
+    gptq_status st = encode_u8_2d(&mw[l], p.layer[l < C::NL ? l : 0].qweight, p.d_col / 2, p.d_row,
+                                  p.d_col / 2, 128, C::ROWS, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != GPTQ_OK) return st;
+  }
+  const uint32_t n = static_cast<uint32_t>(p.n);
+  gptq_status st;
+  if (a.whole) {
+    const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(p.d_col / 128), n};
+    const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(p.ldx)};
+    const cuuint32_t box[3] = {128, w4a8::CPS, n}, estr[3] = {1, 1, 1};
+    CUresult cr = g_encode(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t*>(p.x), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    st = cr == CUDA_SUCCESS ? GPTQ_OK : GPTQ_ERR_CUDA;
+  } else {
+    st = encode_u8_2d(&mx, p.x, p.d_col, n, p.ldx, 128, n, CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  if (st != GPTQ_OK) return st;
   cudaLaunchConfig_t lc{};
   cudaLaunchAttribute at[1];
-  const unsigned tiles = static_cast<unsigned>((p.d_row + w4a8::ROWS - 1) / w4a8::ROWS);
-  const unsigned ctas = (tiles + w4a8::CLUSTER - 1) / w4a8::CLUSTER * w4a8::CLUSTER;
-  const unsigned toks = static_cast<unsigned>((p.n + w4a8::TOK - 1) / w4a8::TOK);
-  lc.gridDim = dim3(p.out == GPTQ_I8 ? ctas : tiles, toks);
+  // whole clusters' worth of tiles for an 8-bit output
+  const unsigned step = p.out == GPTQ_I8 ? C::CLUSTER : 1;
+  const unsigned tiles =
+      (static_cast<unsigned>((p.d_row + C::ROWS - 1) / C::ROWS) + step - 1) / step * step;
+  a.tiles = static_cast<int>(tiles);
   lc.blockDim = dim3(w4a8::THREADS);
+  lc.dynamicSmemBytes = C::SMEM;
   lc.stream = s;
   if (p.out == GPTQ_I8) {
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = w4a8::CLUSTER;
+    at[0].val.clusterDim.x = C::CLUSTER;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
   }
-  const int g = p.group;
-  // a region of 32 RJ columns has one scale: with one scale a row, always;
-  // else it must lie inside a group
-  cudaError_t e;
-  if (p.n_groups == 1 || g % 128 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 4>, p);
-  else if (g % 64 == 0) e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 2>, p);
-  else e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<GATED, 1>, p);
+  // As many CTAs as are on the GPU at once (clusters: fewer than the SMs' room,
+  // as one lies within a GPC; a cluster that has to wait would double the
+  // time), and no more than it takes for the same number of rounds.
+  unsigned most = static_cast<unsigned>(num_sms) * C::MINB;
+  if (step > 1) {
+    static std::atomic<int> resident[64];
+    int dev = 0;
+    GPTQ_CUDA_TRY(cudaGetDevice(&dev));
+    int k = resident[dev].load();
+    if (k == 0) {
+      lc.gridDim = dim3(step);
+      GPTQ_CUDA_TRY(cudaOccupancyMaxActiveClusters(&k, w4a8::w4a8_rows_kernel<C>, &lc));
+      if (k < 1) return GPTQ_ERR_CUDA;
+      resident[dev].store(k);
+    }
+    most = static_cast<unsigned>(k) * step;
+  }
+  const unsigned rounds = (tiles + most - 1) / most;
+  lc.gridDim = dim3((tiles / step + rounds - 1) / rounds * step);
+  cudaError_t e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<C>, mw[0], mw[1], mx, a);
   (void)e;  // also kept for cudaGetLastError, which the check reads
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
+}
+
+template <int NL, int NT>
+gptq_status w4a8_rows(const w4a8::Params& p, int num_sms, cudaStream_t s) {
+  // a region of 32 RJ columns has one scale: with one scale a row, always;
+  // else it must lie inside a group
+  if (p.n_groups == 1 || p.group % 128 == 0) return w4a8_rows_launch<w4a8::Cfg<NL, 4, NT>>(p, num_sms, s);
+  if (p.group % 64 == 0) return w4a8_rows_launch<w4a8::Cfg<NL, 2, NT>>(p, num_sms, s);
+  return w4a8_rows_launch<w4a8::Cfg<NL, 1, NT>>(p, num_sms, s);
 }
 
 template <class C>
@@ -595,7 +691,6 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   const int64_t tiles = w4a8_tiles<C>(p);
   const int nchunks = (p.d_col + w4a8t::CH - 1) / w4a8t::CH;
   a.runs = p.n_groups == 1 || p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-  a.gmagic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.group - 1) / p.group);
   a.wait_ns = g_wait_ns.load();
   a.ksplit = 1;
   if (!C::BIG) {
@@ -669,6 +764,7 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
   p.d_col = static_cast<int>(d_col);
   p.group = cfg->group_size ? cfg->group_size : p.d_col;
   p.n_groups = p.d_col / p.group;
+  p.gmagic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.group - 1) / p.group);
   p.xgroups = x_group ? (p.d_col + 127) / 128 : 1;
   p.out = y_type;
 
@@ -676,9 +772,9 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
   gptq_status st = device_setup(&num_sms);
   if (st != GPTQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n <= w4a8::TOK) return w4a8_rows<GATED>(p, s);
   using Cf = W4a8Cfg<GATED>;
-  if (n <= Cf::Tiny::TN) return w4a8_tiled<typename Cf::Tiny>(p, num_sms, s);
+  if (n <= 8) return w4a8_rows<Cf::NL, 1>(p, num_sms, s);
+  if (n <= 16) return w4a8_rows<Cf::NL, 2>(p, num_sms, s);
   if (n <= Cf::Small::TN) return w4a8_tiled<typename Cf::Small>(p, num_sms, s);
   const int64_t big = w4a8_tiles<typename Cf::Big>(p);
   if (n > Cf::Mid::TN && big >= num_sms) return w4a8_tiled<typename Cf::Big>(p, num_sms, s);

@@ -10,17 +10,23 @@
 // the sum.
 //
 // The contraction runs on mma.sync m16n8k32 (u8 x s8, int32 accumulation)
-// with the weights' rows as M and the tokens as N = 8: at few tokens the pass
-// is bound by reading the packed weights once, and what counts is how little
-// work a word of eight codes costs.  Two ANDs and a shift give its even and
-// odd codes as bytes, which are the k positions of one mma; the activations
-// are permuted to match (two PRMT for eight of them, shared by all row
-// tiles).  The zero points are not subtracted from the codes: an mma of ones
-// gives sum_k x in the same registers as the products, for all row tiles.
+// with the weights' rows as M and the tokens as N = 8 (up to four times): at
+// few tokens the pass is bound by reading the packed weights once, and what
+// counts is bytes in flight and how little work a word of eight codes costs.
+// Two ANDs and a shift give a word's even and odd codes as bytes, which are
+// the k positions of one mma; the activations are permuted to match (two PRMT
+// for eight of them, shared by both row tiles).  The zero points are not
+// subtracted from the codes: an mma of ones gives sum_k x in the same
+// registers as the products, for both row tiles.
 //
-// A CTA has 8 warps and 32 rows of each layer; warp w takes the 128-column
-// chunks w, w + 8, ... and a sum over the warps through shared memory ends
-// the tile, in a fixed order.
+// A CTA has two 16-row tiles: rows of one layer, or the same rows of gate and
+// up.  A producer warp brings stages of eight 128-column chunks into a ring by
+// tensor copies (the tiles' words in boxes of 128 B rows, two chunks each; the
+// tokens' codes in one box where the row is whole chunks), and of each stage
+// warp w computes chunk w.  A sum over the warps through shared memory ends
+// the tile, in a fixed order.  Two CTAs share an SM, with 128 KB of weights on
+// the way, and take tile after tile, so the copies never pause.  Scales and
+// zero points are loaded one chunk ahead.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -35,12 +41,9 @@ namespace w4a8 {
 namespace cg = cooperative_groups;
 
 constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_I8 = 2;  // == GPTQ_F32, GPTQ_BF16, GPTQ_I8
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
-constexpr int WT = 2;           // 16-row tiles of each layer
-constexpr int ROWS = 16 * WT;   // rows of each layer per CTA
-constexpr int TOK = 8;          // tokens per CTA
-constexpr int CLUSTER = 128 / ROWS;  // CTAs that share a block of 128 output columns
+constexpr int WARPS = 8;     // computing warps
+constexpr int THREADS = WARPS * 32 + 32;  // and the producer warp
+constexpr int CPS = WARPS;      // 128-column chunks per stage
 
 struct Layer {
   const uint32_t* qweight;
@@ -58,6 +61,7 @@ struct Params {
   int64_t n;
   int d_row, d_col;
   int group, n_groups;  // of the weights; group = d_col when there is one a row
+  uint32_t gmagic;      // ceil(2^32 / group): umulhi(k, gmagic) == k / group for k, group <= 2^16
   int xgroups;          // 1, or one per 128 columns
   int out;
 };
@@ -83,133 +87,345 @@ __device__ __forceinline__ void store_out(const Params& p, int64_t at, float v) 
   else static_cast<float*>(p.y)[at] = v;
 }
 
-// RJ: runs of 32 columns in a region: 1, 2, or 4 (whole chunks).  With whole
-// chunks the k order inside a chunk is free, and a lane reads 16 bytes of a
-// row (columns 32 t .. 32 t + 31 for lane t of a quad); else word 4 j + t.
-template <bool GATED, int RJ>
-__global__ void __launch_bounds__(THREADS, 2) w4a8_rows_kernel(const Params p) {
-  constexpr int NL = GATED ? 2 : 1;
+// NL: layers; RJ: runs of 32 columns in a region: 1, 2, or 4 (whole chunks);
+// NT: groups of eight tokens; S: stages; MINB: CTAs per SM.
+template <int NL_, int RJ_, int NT_>
+struct Cfg {
+  static constexpr int NL = NL_, RJ = RJ_, NT = NT_;
+  static constexpr int ROWS = NL == 2 ? 16 : 32;  // rows of each layer per CTA
+  static constexpr int CLUSTER = 128 / ROWS;      // CTAs that share 128 output columns
+  static constexpr int W_BYTES = 32 * 128 * CPS / 2;  // both tiles' words of a stage
+  static constexpr int X_BYTES = 8 * NT * 128;        // the tokens' codes of one chunk
+  static constexpr int STAGE_BYTES = W_BYTES + CPS * X_BYTES;
+  static constexpr int MINB = 2;
+  static constexpr int RED_BYTES = WARPS * NT * 32 * 16;  // the warps' sums of one 16-row tile
+  static constexpr int TOP_BYTES = 2 * CLUSTER * 8 * NT * 4;
+  static constexpr int S = (227 * 1024 / MINB - RED_BYTES - TOP_BYTES - 3072) / STAGE_BYTES;
+  static constexpr int SMEM = S * STAGE_BYTES + RED_BYTES + TOP_BYTES + (2 * S + 2) * 8 + 16 +
+                              1024 /* alignment */;
+  static_assert(S >= 2, "stages");
+  static_assert((SMEM + 1024) * MINB <= 228 * 1024, "shared memory");
+};
+
+struct Launch {
+  Params p;
+  uint64_t wait_ns;
+  int tiles;  // blocks of ROWS rows
+  int whole;  // the tokens' map is 3-D: columns of a chunk, chunks, tokens
+};
+
+// Arrive on the barrier at this address of a CTA of the cluster, after the
+// caller's and (through a CTA barrier) its CTA's writes there.
+__device__ __forceinline__ void arrive_peer(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\t"
+      "mapa.shared::cluster.u32 r, %0, %1;\n\t"
+      "fence.acq_rel.cluster;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+// Wait for the peers' arrivals and what they wrote before; bounded.
+__device__ __forceinline__ bool wait_peers(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           uint64_t limit_ns) {
+  const bool ok = mbar_wait_bounded(bar, parity, abort_flag, limit_ns);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
+template <class C>
+__global__ void __launch_bounds__(THREADS, C::MINB)
+w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
+                 const __grid_constant__ CUtensorMap tmap_w1,
+                 const __grid_constant__ CUtensorMap tmap_x, const Launch a) {
+  constexpr int NL = C::NL, RJ = C::RJ, NT = C::NT, S = C::S, ROWS = C::ROWS;
   constexpr int NREG = 4 / RJ;
-  __shared__ float red[WARPS][NL * WT][32][4];
-  __shared__ uint32_t tops[TOK];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int words = p.d_col >> 3;
+  const Params& p = a.p;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (ring - raw);
+  float* red = reinterpret_cast<float*>(base + S * C::STAGE_BYTES);  // [warp][NT][32][4]
+  // maxima of the cluster's CTAs, two sets in turn: [set][rank][token]
+  uint32_t* tops = reinterpret_cast<uint32_t*>(base + S * C::STAGE_BYTES + C::RED_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * S + 2);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, tops0 = empty0 + 8u * S;
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8u * s, 1);
+      mbar_init(empty0 + 8u * s, WARPS);
+    }
+    for (int s = 0; s < 2; ++s) mbar_init(tops0 + 8u * s, C::CLUSTER);
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tmap_w0);
+    if (NL == 2) tma_prefetch_desc(&tmap_w1);
+    tma_prefetch_desc(&tmap_x);
+  }
+  const bool codes = NL == 2 && p.out == OUT_I8;  // then the launch has clusters
+  if (codes) cg::this_cluster().sync();  // the peers' barriers stand before any arrival
+  else __syncthreads();
+
   const int nchunks = (p.d_col + 127) >> 7;
-  const int row0 = blockIdx.x * ROWS;
-  const int64_t tok0 = static_cast<int64_t>(blockIdx.y) * TOK;
-  const int ntok = static_cast<int>(min(static_cast<int64_t>(TOK), p.n - tok0));
+  const int stages = (nchunks + CPS - 1) / CPS;
+  const int ntok = static_cast<int>(p.n);
+  const int g = lane >> 2, t = lane & 3;
+  bool ok = true;
+  uint32_t st = 0, ph = 0;
 
-  float acc[NL * WT][4];
-#pragma unroll
-  for (int i = 0; i < NL * WT; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
-
-  // rows past the layer are computed on its last row and never written;
-  // tokens past the batch are zeros
-  int prow[WT][2];
-#pragma unroll
-  for (int i = 0; i < WT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) prow[i][h] = min(row0 + 16 * i + g + 8 * h, p.d_row - 1);
-  const int8_t* xrow = p.x + (tok0 + (g < ntok ? g : 0)) * p.ldx;
-  const float* xs0 = p.xs + (tok0 + min(2 * t, ntok - 1)) * p.xgroups;
-  const float* xs1 = p.xs + (tok0 + min(2 * t + 1, ntok - 1)) * p.xgroups;
-
-  if (row0 < p.d_row) {
-    for (int c = warp; c < nchunks; c += WARPS) {
-      uint2 xv[4];
-      uint32_t w[NL * WT][2][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // the run of 32 columns that the lane's word j lies in
-        const bool in = 128 * c + 32 * (RJ == 4 ? t : j) < p.d_col;
-        const int word = 16 * c + (RJ == 4 ? 4 * t + j : 4 * j + t);
-        xv[j] = in && g < ntok ? *reinterpret_cast<const uint2*>(xrow + 8 * word) : make_uint2(0u, 0u);
-#pragma unroll
-        for (int i = 0; i < NL * WT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            w[i][h][j] = in ? __ldg(p.layer[i / WT].qweight +
-                                    static_cast<size_t>(prow[i % WT][h]) * words + word)
-                            : 0u;
+  if (warp == WARPS) {
+    // ------------------------------------------------------------ producer
+    uint32_t issued = 0;
+    for (int tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
+      const int row0 = tile * ROWS;
+      if (row0 >= p.d_row) continue;  // fills up the cluster
+      for (int s = 0; s < stages; ++s) {
+        ok = mbar_wait_bounded(empty0 + 8u * st, ph ^ 1u, abort_flag, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t fb = full0 + 8u * st, at = ring + st * C::STAGE_BYTES;
+        const int c0 = s * CPS, nc = min(CPS, nchunks - c0), pairs = (nc + 1) / 2;
+        if (lane == 0)
+          mbar_arrive_expect_tx(fb, pairs * 4096 + (a.whole ? CPS : nc) * ntok * 128);
+        __syncwarp();
+        if (lane < pairs) {  // 32 rows of 128 B each, at 4 KB
+          const int x = (c0 / 2 + lane) * 128;
+          tma_load_2d(at + lane * 4096, &tmap_w0, fb, x, row0);
+          if (NL == 2) tma_load_2d(at + lane * 4096 + 2048, &tmap_w1, fb, x, row0);
+        }
+        if (a.whole) {  // [token][chunk][128 B]
+          if (lane == 8) tma_load_3d(at + C::W_BYTES, &tmap_x, fb, 0, c0, 0);
+        } else if (lane >= 8 && lane < 8 + nc) {  // [chunk][token][128 B]
+          tma_load_2d(at + C::W_BYTES + (lane - 8) * C::X_BYTES, &tmap_x, fb, (c0 + lane - 8) * 128, 0);
+        }
+        __syncwarp();
+        ++issued;
+        if (++st == S) { st = 0; ph ^= 1u; }
       }
-      const int cx = p.xgroups == 1 ? 0 : c;
-      const float sx0 = __ldg(xs0 + cx), sx1 = __ldg(xs1 + cx);
+    }
+    if (!ok && lane == 0) {  // given up: no copy may land in memory that is handed on
+      int own = 0;
+      for (uint32_t k = 0; k < S && k < issued; ++k) {
+        const uint32_t i = issued - 1 - k;
+        mbar_wait_bounded(full0 + 8u * (i % S), (i / S) & 1u, &own, a.wait_ns);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- compute
+    float acc[2][NT][4];
+    const float* sp[2][2];
+    const uint8_t* zp[2][2];
+    uint32_t set = 0;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    const int row0 = tile * ROWS;
+    // rows past the layer take its last row's scales and are never written
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = min(row0 + (NL == 2 ? 0 : 16 * i) + g + 8 * h, p.d_row - 1);
+        const Layer& L = p.layer[NL == 2 ? i : 0];
+        sp[i][h] = L.scales + static_cast<size_t>(row) * p.n_groups;
+        zp[i][h] = L.zeros + static_cast<size_t>(row) * p.n_groups;
+      }
+    struct Scales {
+      float sx[NT][2], s[2][2][NREG];
+      uint32_t z[2][2][NREG];
+    };
+    auto load = [&](int c, Scales& k) {
+      const int cx = p.xgroups == 1 ? 0 : min(c, nchunks - 1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          k.sx[n][e] = __ldg(p.xs + static_cast<int64_t>(min(8 * n + 2 * t + e, ntok - 1)) * p.xgroups + cx);
 #pragma unroll
       for (int m = 0; m < NREG; ++m) {
-        if (128 * c + 32 * RJ * m >= p.d_col) break;
-        const int gi = (128 * c + 32 * RJ * m) / p.group;
-        int sums[4] = {0, 0, 0, 0};
-        uint32_t b0[RJ], b1[RJ];
+        const int gi =
+            min(static_cast<int>(__umulhi(128 * c + 32 * RJ * m, p.gmagic)), p.n_groups - 1);
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-          b0[j] = __byte_perm(xv[RJ * m + j].x, xv[RJ * m + j].y, 0x6420);
-          b1[j] = __byte_perm(xv[RJ * m + j].x, xv[RJ * m + j].y, 0x7531);
-          mma_u8s8(sums, 0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u, b0[j], b1[j]);
-        }
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < NL * WT; ++i) {
-          int prod[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < RJ; ++j) {
-            const uint32_t vg = w[i][0][RJ * m + j], vh = w[i][1][RJ * m + j];
-            mma_u8s8(prod, even_codes(vg), even_codes(vh), odd_codes(vg), odd_codes(vh), b0[j], b1[j]);
+          for (int h = 0; h < 2; ++h) {
+            k.s[i][h][m] = __ldg(sp[i][h] + gi);
+            k.z[i][h][m] = __ldg(zp[i][h] + gi);
           }
-          const Layer& L = p.layer[i / WT];
-          const size_t og = static_cast<size_t>(prow[i % WT][0]) * p.n_groups + gi;
-          const size_t oh = static_cast<size_t>(prow[i % WT][1]) * p.n_groups + gi;
-          const float sg = __ldg(L.scales + og), sh = __ldg(L.scales + oh);
-          const int zg = __ldg(L.zeros + og), zh = __ldg(L.zeros + oh);
-          acc[i][0] = fmaf(sg * sx0, static_cast<float>(prod[0] - zg * sums[0]), acc[i][0]);
-          acc[i][1] = fmaf(sg * sx1, static_cast<float>(prod[1] - zg * sums[1]), acc[i][1]);
-          acc[i][2] = fmaf(sh * sx0, static_cast<float>(prod[2] - zh * sums[2]), acc[i][2]);
-          acc[i][3] = fmaf(sh * sx1, static_cast<float>(prod[3] - zh * sums[3]), acc[i][3]);
+      }
+    };
+    // One chunk; with whole chunks the scales of the warp's next one are on
+    // the way meanwhile, into registers of their own: a copy would wait.
+    auto chunk = [&](int c, int slot, Scales& k, Scales& knext) {
+      if (RJ == 4) load(c + WARPS, knext);
+      else load(c, k);
+      if (__all_sync(0xffffffffu, ok) && c < nchunks) {
+        // 128-byte swizzle: 16-byte piece q of row r lies at q ^ (r & 7)
+        const uint8_t* wt = base + st * C::STAGE_BYTES + (slot >> 1) * 4096 + g * 128;
+        const int q0 = 4 * (slot & 1);
+        const uint8_t* xt = base + st * C::STAGE_BYTES + C::W_BYTES +
+                            (a.whole ? g * (CPS * 128) + slot * 128 : slot * C::X_BYTES + g * 128);
+        const int xg = a.whole ? 8 * CPS * 128 : 1024, xr = a.whole ? slot & 7 : g;
+        uint32_t w[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* from = wt + (16 * i + 8 * h) * 128;
+            if (RJ == 4) {  // words 4 t .. 4 t + 3: the k order inside a chunk is free
+              const uint4 v = *reinterpret_cast<const uint4*>(from + (((q0 + t) ^ g) << 4));
+              w[i][h][0] = v.x; w[i][h][1] = v.y; w[i][h][2] = v.z; w[i][h][3] = v.w;
+            } else {  // word 4 j + t
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[i][h][j] = *reinterpret_cast<const uint32_t*>(from + (((q0 + j) ^ g) << 4) + 4 * t);
+            }
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint2 x[4];  // the activations of the lane's words
+          const uint8_t* from = xt + n * xg;
+          if (RJ == 4) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint4 v = *reinterpret_cast<const uint4*>(from + (((2 * t + j) ^ xr) << 4));
+              x[2 * j] = make_uint2(v.x, v.y);
+              x[2 * j + 1] = make_uint2(v.z, v.w);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[j] = *reinterpret_cast<const uint2*>(from + (((2 * j + (t >> 1)) ^ xr) << 4) + 8 * (t & 1));
+          }
+          uint32_t b0[4], b1[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            b0[j] = __byte_perm(x[j].x, x[j].y, 0x6420);
+            b1[j] = __byte_perm(x[j].x, x[j].y, 0x7531);
+          }
+#pragma unroll
+          for (int m = 0; m < NREG; ++m) {
+            int sums[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = RJ * m; j < RJ * m + RJ; ++j)
+              mma_u8s8(sums, 0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u, b0[j], b1[j]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              int prod[4] = {0, 0, 0, 0};
+#pragma unroll
+              for (int j = RJ * m; j < RJ * m + RJ; ++j)
+                mma_u8s8(prod, even_codes(w[i][0][j]), even_codes(w[i][1][j]), odd_codes(w[i][0][j]),
+                         odd_codes(w[i][1][j]), b0[j], b1[j]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[i][n][e] = fmaf(k.s[i][e >> 1][m] * k.sx[n][e & 1],
+                                    static_cast<float>(prod[e] - static_cast<int>(k.z[i][e >> 1][m]) * sums[e]),
+                                    acc[i][n][e]);
+            }
+          }
         }
       }
+    };
+    auto stage = [&](int s, Scales& k, Scales& knext) {
+      if (s >= stages) return;
+      ok = ok && mbar_wait_bounded(full0 + 8u * st, ph, abort_flag, a.wait_ns);
+      chunk(s * CPS + warp, warp, k, knext);
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
+      if (++st == S) { st = 0; ph ^= 1u; }
+    };
+    if (row0 < p.d_row) {
+      Scales k0, k1;
+      if (RJ == 4) load(warp, k0);
+      for (int s = 0; s < stages; s += 2) {
+        stage(s, k0, k1);
+        stage(s + 1, k1, k0);
+      }
     }
-  }
 
-  // Sum over the warps.  Element e of lane l of a fragment is row
-  // (l >> 2) + 8 (e >> 1) of the 16-row tile, token 2 (l & 3) + (e & 1).
+    // The sums over the warps, one 16-row tile at a time; a thread gets the
+    // outputs tid, tid + 256, ... of 16 rows x 8 NT tokens.  Element e of lane
+    // l of a fragment is row (l >> 2) + 8 (e >> 1) of its tile, token
+    // 2 (l & 3) + (e & 1) of its group of eight.
+    constexpr int OUTS = (16 * 8 * NT + 32 * WARPS - 1) / (32 * WARPS);
+    float v[2][OUTS];
 #pragma unroll
-  for (int i = 0; i < NL * WT; ++i)
+    for (int i = 0; i < 2; ++i) {
+      named_bar(1, 32 * WARPS);  // the last sums have been read
 #pragma unroll
-    for (int e = 0; e < 4; ++e) red[warp][i][lane][e] = acc[i][e];
-  __syncthreads();
-  const int rl = threadIdx.x & 31, tk = threadIdx.x >> 5;  // one output each
-  const int fl = (rl & 7) * 4 + (tk >> 1), fe = 2 * ((rl >> 3) & 1) + (tk & 1);
-  float v[NL];
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float4*>(red + ((warp * NT + n) * 32 + lane) * 4) =
+            make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
+      named_bar(1, 32 * WARPS);
 #pragma unroll
-  for (int a = 0; a < NL; ++a) {
-    v[a] = 0.0f;
+      for (int j = 0; j < OUTS; ++j) {
+        const int o = threadIdx.x + j * 32 * WARPS, rl = o & 15, tk = o >> 4;
+        v[i][j] = 0.0f;
+        if (tk < ntok)
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) v[a] += red[w][a * WT + (rl >> 4)][fl][fe];
-  }
-  const bool live = row0 + rl < p.d_row && tk < ntok;
-  const float out = GATED ? silu_times(v[0], v[NL - 1]) : v[0];
-  if (!GATED || p.out != OUT_I8) {
-    if (live) store_out(p, (tok0 + tk) * p.ldy + row0 + rl, out);
-    return;
-  }
-  if constexpr (GATED) {
-    // 8-bit output: a warp has one token's 32 rows; the CTAs of the cluster
-    // exchange their maxima over the block of 128 output columns
-    cg::cluster_group cl = cg::this_cluster();
-    uint32_t top = __reduce_max_sync(0xffffffffu, live ? act8::abs_bits(out) : 0u);
-    if (rl == 0) tops[tk] = top;
-    cl.sync();
-    for (int r = 0; r < CLUSTER; ++r) top = max(top, *cl.map_shared_rank(&tops[tk], r));
-    const act8::Quant q = act8::quant_of(top);
-    if (live) {
-      static_cast<int8_t*>(p.y)[(tok0 + tk) * p.ldy + row0 + rl] =
-          static_cast<int8_t>(act8::code_or_zero(out, q));
-      if (row0 % 128 == 0 && rl == 0)
-        p.ys[(tok0 + tk) * ((p.d_row + 127) / 128) + row0 / 128] = q.scale;
+          for (int w = 0; w < WARPS; ++w)
+            v[i][j] += red[((w * NT + (tk >> 3)) * 32 + (rl & 7) * 4 + ((tk & 7) >> 1)) * 4 +
+                           2 * (rl >> 3) + (tk & 1)];
+      }
     }
-    cl.sync();  // no CTA leaves while another may still read its maxima
+    if (NL == 1 || !codes) {
+#pragma unroll
+      for (int j = 0; j < OUTS; ++j) {
+        const int o = threadIdx.x + j * 32 * WARPS, row = row0 + (o & 15), tk = o >> 4;
+        if (tk >= ntok) continue;
+        if (NL == 2) {
+          if (row < p.d_row) store_out(p, tk * p.ldy + row, silu_times(v[0][j], v[1][j]));
+        } else {
+          if (row < p.d_row) store_out(p, tk * p.ldy + row, v[0][j]);
+          if (row + 16 < p.d_row) store_out(p, tk * p.ldy + row + 16, v[1][j]);
+        }
+      }
+    } else {
+      // 8-bit output: half a warp has a token's 16 rows; each CTA of the
+      // cluster tells the others its maxima over the block of 128 columns.  A
+      // set is free again when it comes round: a peer that writes it for the
+      // next tile but one has seen this CTA's arrival for the next.
+      const uint32_t at = set & 1u;
+      float h[OUTS];
+      cg::cluster_group cl = cg::this_cluster();
+      const uint32_t rank = cl.block_rank();
+#pragma unroll
+      for (int j = 0; j < OUTS; ++j) {
+        const int o = threadIdx.x + j * 32 * WARPS, tk = o >> 4;
+        const bool live = tk < ntok && row0 + (o & 15) < p.d_row;
+        h[j] = live ? silu_times(v[0][j], v[1][j]) : 0.0f;
+        const uint32_t top =
+            __reduce_max_sync(lane & 16 ? 0xffff0000u : 0x0000ffffu, act8::abs_bits(h[j]));
+        if (tk < ntok && (lane & 15) < C::CLUSTER)  // a lane a peer
+          *cl.map_shared_rank(&tops[(at * C::CLUSTER + rank) * 8 * NT + tk], lane & 15) = top;
+      }
+      named_bar(1, 32 * WARPS);
+      if (threadIdx.x < C::CLUSTER) arrive_peer(tops0 + 8u * at, threadIdx.x);
+      ok = ok && wait_peers(tops0 + 8u * at, (set >> 1) & 1u, abort_flag, a.wait_ns);
+      ++set;
+#pragma unroll
+      for (int j = 0; j < OUTS; ++j) {
+        const int o = threadIdx.x + j * 32 * WARPS, tk = o >> 4, row = row0 + (o & 15);
+        if (tk >= ntok || row >= p.d_row) continue;
+        uint32_t top = 0;
+#pragma unroll
+        for (int r = 0; r < C::CLUSTER; ++r) top = max(top, tops[(at * C::CLUSTER + r) * 8 * NT + tk]);
+        const act8::Quant q = act8::quant_of(top);
+        static_cast<int8_t*>(p.y)[tk * p.ldy + row] = static_cast<int8_t>(act8::code_or_zero(h[j], q));
+        if (row % 128 == 0) p.ys[tk * static_cast<int64_t>((p.d_row + 127) / 128) + row / 128] = q.scale;
+      }
+    }
+    }
   }
+  __syncthreads();
+  if (codes) cg::this_cluster().sync();  // no CTA leaves while another may still write its maxima
 }
 
 }  // namespace w4a8

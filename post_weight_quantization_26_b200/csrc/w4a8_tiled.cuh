@@ -81,7 +81,6 @@ struct Tiled {
   int row_tiles, tok_tiles;
   int ksplit;        // CTAs of a cluster along the columns
   int runs;          // runs per chunk: 4 (32 columns), 2, or 1
-  uint32_t gmagic;   // ceil(2^32 / group): umulhi(k, gmagic) == k / group for k, group <= 2^16
   uint64_t wait_ns;
 };
 
@@ -230,7 +229,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   // a chunk's last run closes its TMEM buffer unless neither scale changes
   const bool every = p.xgroups != 1 || a.runs != 1 || p.group == CH;
   auto group_of = [&](int col) {
-    return min(static_cast<int>(__umulhi(static_cast<uint32_t>(col), a.gmagic)), p.n_groups - 1);
+    return min(static_cast<int>(__umulhi(static_cast<uint32_t>(col), p.gmagic)), p.n_groups - 1);
   };
   auto closes = [&](int c) {
     return every || c == c1 - 1 || group_of((c + 1) * CH) != group_of(c * CH);
