@@ -691,6 +691,10 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   const int64_t tiles = w4a8_tiles<C>(p);
   const int nchunks = (p.d_col + w4a8t::CH - 1) / w4a8t::CH;
   a.runs = p.n_groups == 1 || p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
+  a.xvec = p.xgroups % 4 == 0 && aligned(p.xs, 16);
+  a.wvec = p.n_groups % 4 == 0;
+  for (int l = 0; l < C::NL; ++l)
+    a.wvec = a.wvec && aligned(p.layer[l].scales, 16) && aligned(p.layer[l].zeros, 4);
   a.wait_ns = g_wait_ns.load();
   a.ksplit = 1;
   if (!C::BIG) {

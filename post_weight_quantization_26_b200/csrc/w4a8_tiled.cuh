@@ -62,9 +62,10 @@ struct Cfg {
   static constexpr int SUM_BYTES = BIG ? 0 : NL * TN * BM * 4;  // over the ring, at the end
   static constexpr int SX_BYTES = 2 * 4 * TN * 4;       // two sets of token scales
   static constexpr int SW_BYTES = 2 * 4 * NL * BM * 4;  // two sets of row scales
+  static constexpr int Z_BYTES = 2 * NL * BM * 4;       // and of zero points, four in a word
   static constexpr int TOP_BYTES = BIG ? 4 * TN * 4 : 0;
   static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 5;
-  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + TOP_BYTES +
+  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + Z_BYTES + TOP_BYTES +
                               BARS * 8 + 16 + 1024 /* alignment */;
   static_assert(NU >= NL && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
@@ -81,6 +82,7 @@ struct Tiled {
   int row_tiles, tok_tiles;
   int ksplit;        // CTAs of a cluster along the columns
   int runs;          // runs per chunk: 4 (32 columns), 2, or 1
+  int xvec, wvec;    // rows of token scales, and of row scales and zero points, allow vector loads
   uint64_t wait_ns;
 };
 
@@ -175,7 +177,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   const uint32_t slots = ring + C::RING_BYTES;
   float* sx = reinterpret_cast<float*>(base + C::RING_BYTES + AS * SLOT_BYTES);
   float* swb = sx + C::SX_BYTES / 4;
-  uint32_t* tops = reinterpret_cast<uint32_t*>(swb + C::SW_BYTES / 4);
+  uint32_t* zb = reinterpret_cast<uint32_t*>(swb + C::SW_BYTES / 4);
+  uint32_t* tops = zb + C::Z_BYTES / 4;
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -201,7 +204,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(sfull0 + 8u * u, 2);
-      mbar_init(sempty0 + 8u * u, EW);
+      mbar_init(sempty0 + 8u * u, UW + EW);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -331,53 +334,74 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       }
     } else {
       // --------------------------------------------------------- scale warps
-      // The scales of the next runs, in sets of four runs (4, 2 or 1 chunks):
-      // their row scales, and their chunks' token scales.
+      // The scales and zero points of the next runs, in sets of four runs (4,
+      // 2 or 1 chunks), and those chunks' token scales.  A lane reads a row's
+      // or token's four at once where they lie in 16 aligned bytes: one value
+      // at a time, 32 lines a load, the reads took more of the load unit than
+      // all else in the kernel (640 clocks a chunk of 128 x 256 outputs).
       const int i = threadIdx.x - (UW + EW + 2) * 32;  // 0..63
       const int per_set = 4 / a.runs, step = CH / a.runs;
+      constexpr int TK = (TN + 63) / 64;  // tokens of a thread
       uint32_t set = 0;
       for (int64_t t = tile0; t < tiles; t += tile_step) {
         const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
         const int64_t tok0 = (t % a.tok_tiles) * TN;
         for (int cs = c0; cs < c1; cs += per_set, ++set) {
-          int gi[4], ci[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            gi[j] = group_of(cs * CH + j * step);
-            ci[j] = p.xgroups == 1 ? 0 : min(cs + j, nchunks - 1);
-          }
           const uint32_t at = set & 1u;
-          W4T_WAIT(sempty0 + 8u * at, ((set >> 1) & 1u) ^ 1u);
-          float* xo = sx + at * 4 * TN;
-          float* wo = swb + at * NL * 4 * BM;
-#pragma unroll
-          for (int l = 0; l < NL; ++l) {
-            float v[BM / 64][4];
-#pragma unroll
-            for (int k = 0; k < BM / 64; ++k) {
-              const float* from = p.layer[l].scales +
-                                  static_cast<size_t>(min(row0 + i + 64 * k, p.d_row - 1)) * p.n_groups;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[k][j] = __ldg(from + gi[j]);
-            }
-#pragma unroll
-            for (int k = 0; k < BM / 64; ++k)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) wo[(l * 4 + j) * BM + i + 64 * k] = v[k][j];
-          }
-          constexpr int TK = (TN + 63) / 64;  // tokens of a thread
-          float v[TK][4];
+          float4 x[TK];
+          const bool xvec = a.xvec && (cs & 3) == 0 && cs + 4 <= p.xgroups;
 #pragma unroll
           for (int k = 0; k < TK; ++k) {
             const float* from = p.xs + min(tok0 + i + 64 * k, p.n - 1) * p.xgroups;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[k][j] = __ldg(from + ci[j]);
+            if (xvec) {
+              x[k] = __ldg(reinterpret_cast<const float4*>(from + cs));
+            } else if (p.xgroups == 1) {
+              x[k].x = x[k].y = x[k].z = x[k].w = __ldg(from);
+            } else {
+              x[k].x = __ldg(from + cs);
+              x[k].y = __ldg(from + min(cs + 1, nchunks - 1));
+              x[k].z = __ldg(from + min(cs + 2, nchunks - 1));
+              x[k].w = __ldg(from + min(cs + 3, nchunks - 1));
+            }
           }
+          const int g0 = group_of(cs * CH), g1 = group_of(cs * CH + step),
+                    g2 = group_of(cs * CH + 2 * step), g3 = group_of(cs * CH + 3 * step);
+          const bool wvec = a.wvec && (g0 & 3) == 0 && g3 == g0 + 3;
+          W4T_WAIT(sempty0 + 8u * at, ((set >> 1) & 1u) ^ 1u);
+#pragma unroll
+          for (int l = 0; l < NL; ++l)
+#pragma unroll
+            for (int k = 0; k < BM / 64; ++k) {
+              const int r = i + 64 * k;
+              const size_t first = static_cast<size_t>(min(row0 + r, p.d_row - 1)) * p.n_groups;
+              const float* sf = p.layer[l].scales + first;
+              const uint8_t* zf = p.layer[l].zeros + first;
+              float4 v;
+              uint32_t z;
+              if (wvec) {
+                v = __ldg(reinterpret_cast<const float4*>(sf + g0));
+                z = __ldg(reinterpret_cast<const uint32_t*>(zf + g0));
+              } else {
+                v = make_float4(__ldg(sf + g0), __ldg(sf + g1), __ldg(sf + g2), __ldg(sf + g3));
+                z = __ldg(zf + g0) | (__ldg(zf + g1) << 8) | (__ldg(zf + g2) << 16) |
+                    (static_cast<uint32_t>(__ldg(zf + g3)) << 24);
+              }
+              float* wo = swb + (at * NL + l) * 4 * BM + r;
+              wo[0] = v.x;
+              wo[BM] = v.y;
+              wo[2 * BM] = v.z;
+              wo[3 * BM] = v.w;
+              zb[(at * NL + l) * BM + r] = z;
+            }
+          float* xo = sx + at * 4 * TN + i;
 #pragma unroll
           for (int k = 0; k < TK; ++k)
-            if (TN % 64 == 0 || i + 64 * k < TN)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) xo[j * TN + i + 64 * k] = v[k][j];
+            if (TN % 64 == 0 || i + 64 * k < TN) {
+              xo[64 * k] = x[k].x;
+              xo[TN + 64 * k] = x[k].y;
+              xo[2 * TN + 64 * k] = x[k].z;
+              xo[3 * TN + 64 * k] = x[k].w;
+            }
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(sfull0 + 8u * at);
         }
@@ -390,30 +414,17 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     constexpr int PIECES = 16 / UW;        // 16-byte pieces (32 codes) of a thread
     const int i0 = (threadIdx.x / BM) * PIECES;
     const uint32_t in_row = r * 64, out_row = r * 128;
-    uint32_t st = 0, ph = 0, slot = 0, sph = 0;
+    uint32_t st = 0, ph = 0, slot = 0, sph = 0, set = 0;
+    const int per_set = 4 / a.runs;
     for (int64_t t = tile0; t < tiles; t += tile_step) {
-      const int row = min(static_cast<int>(t / a.tok_tiles) * BM + r, p.d_row - 1);
-      const uint8_t* zr[NL];
+      for (int cs = c0; cs < c1; cs += per_set, ++set) {
+        const uint32_t at = set & 1u;
+        W4T_WAIT(sfull0 + 8u * at, (set >> 1) & 1u);
+        uint32_t z[NL];  // four zero points of the row
 #pragma unroll
-      for (int l = 0; l < NL; ++l) zr[l] = p.layer[l].zeros + static_cast<size_t>(row) * p.n_groups;
-      // Zero points come four at a time, one set ahead: of four chunks, or of
-      // one chunk's runs of 32 columns where a run may end inside it.
-      const bool fine = a.runs != 1;
-      const int per_set = fine ? 1 : 4, zstep = fine ? 32 : CH;
-      uint32_t znext[NL][4];
-      auto load_z = [&](int c) {
-#pragma unroll
-        for (int l = 0; l < NL; ++l)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) znext[l][j] = __ldg(zr[l] + group_of(c * CH + j * zstep));
-      };
-      load_z(c0);
-      for (int cs = c0; cs < c1; cs += per_set) {
-        uint32_t z[NL];  // a byte each
-#pragma unroll
-        for (int l = 0; l < NL; ++l)
-          z[l] = znext[l][0] | (znext[l][1] << 8) | (znext[l][2] << 16) | (znext[l][3] << 24);
-        load_z(cs + per_set);
+        for (int l = 0; l < NL; ++l) z[l] = zb[(at * NL + l) * BM + r];
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(sempty0 + 8u * at);
         const int ce = min(cs + per_set, c1);
 #pragma unroll 1
         for (int c = cs; c < ce; ++c) {
@@ -421,7 +432,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           const uint8_t* in = base + st * C::STAGE_BYTES + in_row;
 #pragma unroll
           for (int l = 0; l < NL; ++l) {
-            const uint32_t zc = __byte_perm(z[l], 0, (c - cs) * 0x1111);  // a chunk's only one
+            const uint32_t first = (c - cs) * a.runs;  // the chunk's first run in the set
             uint4 w[PIECES];
 #pragma unroll
             for (int i = 0; i < PIECES; ++i)
@@ -432,7 +443,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (ok) {
 #pragma unroll
               for (int i = 0; i < PIECES; ++i) {
-                const uint32_t zi = fine ? __byte_perm(z[l], 0, (i0 + i) * 0x1111) : zc;
+                const uint32_t zi = __byte_perm(z[l], 0, (first + ((i0 + i) * a.runs >> 2)) * 0x1111);
                 const uint2 b0 = unpack_word(w[i].x, zi), b1 = unpack_word(w[i].y, zi);
                 const uint2 b2 = unpack_word(w[i].z, zi), b3 = unpack_word(w[i].w, zi);
                 *reinterpret_cast<uint4*>(out + (((2 * (i0 + i)) ^ (r & 7)) << 4)) =
