@@ -91,7 +91,7 @@ struct DeviceInfo {
 template <bool GATED>
 struct W4a8Cfg {
   static constexpr int NL = GATED ? 2 : 1;
-  using Small = w4a8t::Cfg<NL, 64 / NL, 4, GATED ? 4 : 8, GATED ? 3 : 4, 2, 2, false>;
+  using Small = w4a8t::Cfg<NL, 64 / NL, 4, 8 / NL, GATED ? 3 : 4, 2, GATED ? 1 : 2, false>;
   using Mid = w4a8t::Cfg<NL, 128 / NL, 4, 8, 5, GATED ? 4 : 3, 1, false>;
   using Big = w4a8t::Cfg<NL, 256 / NL, 8, 16, 4, GATED ? 4 : 3, 1, true>;
 };
@@ -691,6 +691,8 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   const int64_t tiles = w4a8_tiles<C>(p);
   const int nchunks = (p.d_col + w4a8t::CH - 1) / w4a8t::CH;
   a.runs = p.n_groups == 1 || p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
+  const int64_t ysize = p.out == GPTQ_F32 ? 4 : p.out == GPTQ_BF16 ? 2 : 1;
+  a.yvec = aligned(p.y, p.out == GPTQ_I8 ? 8 : 16) && (p.ldy * ysize) % (p.out == GPTQ_I8 ? 8 : 16) == 0;
   a.xvec = p.xgroups % 4 == 0 && aligned(p.xs, 16);
   a.wvec = p.n_groups % 4 == 0;
   for (int l = 0; l < C::NL; ++l)

@@ -43,6 +43,7 @@ constexpr int BM = 128;  // layer rows per tile
 constexpr int CH = 128;  // columns per chunk
 constexpr int PACKED_BYTES = BM * CH / 2;
 constexpr int SLOT_BYTES = BM * CH;
+constexpr int SUM_PITCH = BM + 4;  // rows of a token's sums: spreads a warp's 8 rows x 4 tokens
 
 // NL: layers; TN: tokens per tile; UW, EW: unpack and epilogue warps; S: ring
 // stages; AS: operand slots of one layer and chunk; MINB: CTAs per SM.  Four
@@ -59,7 +60,7 @@ struct Cfg {
   static constexpr int X_BYTES = TN * CH;
   static constexpr int STAGE_BYTES = NL * PACKED_BYTES + X_BYTES;
   static constexpr int RING_BYTES = S * STAGE_BYTES;
-  static constexpr int SUM_BYTES = BIG ? 0 : NL * TN * BM * 4;  // over the ring, at the end
+  static constexpr int SUM_BYTES = BIG ? 0 : NL * TN * SUM_PITCH * 4;  // over the ring, at the end
   static constexpr int SX_BYTES = 2 * 4 * TN * 4;       // two sets of token scales
   static constexpr int SW_BYTES = 2 * 4 * NL * BM * 4;  // two sets of row scales
   static constexpr int Z_BYTES = 2 * NL * BM * 4;       // and of zero points, four in a word
@@ -69,7 +70,7 @@ struct Cfg {
                               BARS * 8 + 16 + 1024 /* alignment */;
   static_assert(NU >= NL && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
-  static_assert(EW % 4 == 0 && UW % 4 == 0 && COLS % 16 == 0, "warps");
+  static_assert(EW % 4 == 0 && UW % 4 == 0 && COLS % 32 == 0, "warps");
   static_assert((SMEM + 1024) * MINB <= 228 * 1024, "shared memory");
   // BIG moves registers between warpgroups: the launch's are THREADS x LAUNCH
   static constexpr int LAUNCH = 65536 / THREADS / 8 * 8, MORE = 96,
@@ -82,6 +83,7 @@ struct Tiled {
   int row_tiles, tok_tiles;
   int ksplit;        // CTAs of a cluster along the columns
   int runs;          // runs per chunk: 4 (32 columns), 2, or 1
+  int yvec;          // eight rows of an output are aligned for one store
   int xvec, wvec;    // rows of token scales, and of row scales and zero points, allow vector loads
   uint64_t wait_ns;
 };
@@ -137,25 +139,104 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// One run's sums of COLS tokens from TMEM, scaled and added to acc.  The
-// conversion to fp32 is an instruction of half the adders' rate; the add of
-// 1.5 * 2^23 and its subtraction would cost as much and more issue slots.
+// 16 lanes x 32 columns of TMEM: register 4 b + 2 i + e of lane t has row
+// t / 4 + 8 i, column 8 b + 2 (t % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A thread's share of 32 rows x COLS tokens: rows lane / 4 + 8 i + 16 h, and
+// of each eight tokens two.  acc[((p 2 + h) 4 + b) 2 + i] has the tokens
+// 32 p + 8 b + 2 (lane % 4) + {0, 1} of row (h, i).  With four rows a thread
+// needs a quarter of the tokens' scales: one row a thread and all tokens read
+// 128 B a warp and value from shared memory, 620 clocks a chunk of 128 x 256
+// outputs.
 template <int COLS>
-__device__ __forceinline__ void fold_run(uint64_t (&acc)[COLS / 2], uint32_t t0, float sw,
+struct Share {
+  uint64_t v[COLS / 2];
+  __device__ __forceinline__ float at(int p, int h, int b, int i, int e) const {
+    const float2 f = unpack2(v[((p * 2 + h) * 4 + b) * 2 + i]);
+    return e ? f.y : f.x;
+  }
+};
+
+// Transpose 8 values of the 8 lanes with one lane % 4: lane / 4 = j gets value
+// j of each, in the order of the lanes.
+__device__ __forceinline__ void transpose8(float (&v)[8]) {
+  const int j = (threadIdx.x >> 2) & 7;
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & s)) {
+        const bool up = j & s;
+        const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i | s], s << 2);
+        if (up) v[i] = got;
+        else v[i | s] = got;
+      }
+}
+
+// Eight consecutive rows of a token, `left` of them inside the layer; vec: 16-
+// byte (8-bit codes: 8-byte) stores are aligned.
+__device__ __forceinline__ void store_rows8(const Params& p, int64_t at, const float (&v)[8],
+                                            int left, bool vec, const act8::Quant& q) {
+  if (vec && left >= 8) {
+    if (p.out == w4a8::OUT_I8) {
+      *reinterpret_cast<uint2*>(static_cast<int8_t*>(p.y) + at) = act8::codes8(v, q);
+    } else if (p.out == w4a8::OUT_BF16) {
+      float w[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+      act8::store8(static_cast<__nv_bfloat16*>(p.y) + at, w);
+    } else {
+      float w[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+      act8::store8(static_cast<float*>(p.y) + at, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i >= left) break;
+    if (p.out == w4a8::OUT_I8)
+      static_cast<int8_t*>(p.y)[at + i] = static_cast<int8_t>(act8::code_or_zero(v[i], q));
+    else
+      w4a8::store_out(p, at + i, v[i]);
+  }
+}
+
+// One run's sums, scaled and added; t0: the warp's lanes and first column in
+// TMEM, sw: its four rows' scales, sx: the first token's scale.  The conversion
+// to fp32 is an instruction of half the adders' rate; the add of 1.5 * 2^23
+// and its subtraction would cost as much and more issue slots.
+template <int COLS>
+__device__ __forceinline__ void fold_run(Share<COLS>& acc, uint32_t t0, const float (&sw)[4],
                                          const float* sx) {
-  const uint64_t sw2 = pack2(sw, sw);
+  const float* sxt = sx + 2 * (threadIdx.x & 3);
 #pragma unroll
-  for (int b = 0; b < COLS / 16; ++b) {
-    uint32_t v[16];
-    tmem_ld_32x32b_x16(t0 + 16 * b, v);
-    tmem_ld_wait();
+  for (int p = 0; p < COLS / 32; ++p) {
+    uint64_t s[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 s = *reinterpret_cast<const float4*>(sx + 16 * b + 4 * q);
-      const uint64_t f0 = pack2(__int2float_rn(v[4 * q]), __int2float_rn(v[4 * q + 1]));
-      const uint64_t f1 = pack2(__int2float_rn(v[4 * q + 2]), __int2float_rn(v[4 * q + 3]));
-      acc[8 * b + 2 * q] = fma2(f0, mul2(sw2, pack2(s.x, s.y)), acc[8 * b + 2 * q]);
-      acc[8 * b + 2 * q + 1] = fma2(f1, mul2(sw2, pack2(s.z, s.w)), acc[8 * b + 2 * q + 1]);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t v[16];
+      tmem_ld_16x256b_x4(t0 + (static_cast<uint32_t>(16 * h) << 16) + 32 * p, v);
+      if (h == 0)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) s[b] = *reinterpret_cast<const uint64_t*>(sxt + 32 * p + 8 * b);
+      tmem_ld_wait();
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t f = pack2(__int2float_rn(static_cast<int>(v[4 * b + 2 * i])),
+                                   __int2float_rn(static_cast<int>(v[4 * b + 2 * i + 1])));
+          uint64_t& a = acc.v[((p * 2 + h) * 4 + b) * 2 + i];
+          a = fma2(f, mul2(pack2(sw[2 * h + i], sw[2 * h + i]), s[b]), a);
+        }
     }
   }
 }
@@ -474,17 +555,17 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     for (int64_t t = tile0; t < tiles; t += tile_step) {
       const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
       const int64_t tok0 = (t % a.tok_tiles) * TN;
-      const int row = row0 + quarter * 32 + lane;
-      uint64_t acc[NL][COLS / 2];
+      const int row_t = quarter * 32 + (lane >> 2);  // + 8 i + 16 h
+      Share<COLS> acc[NL];
 #pragma unroll
       for (int l = 0; l < NL; ++l)
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) acc[l][j] = 0ull;
+        for (int j = 0; j < COLS / 2; ++j) acc[l].v[j] = 0ull;
       for (int cs = c0; cs < c1; cs += per_set, ++set) {
         const uint32_t at = set & 1u;
         W4T_WAIT(sfull0 + 8u * at, (set >> 1) & 1u);
         const float* sxs = sx + at * 4 * TN + half * COLS;
-        const float* sws = swb + at * NL * 4 * BM + quarter * 32 + lane;
+        const float* sws = swb + at * NL * 4 * BM + row_t;
         const int ce = min(cs + per_set, c1);
 #pragma unroll 1
         for (int c = cs; c < ce; ++c, sxs += TN) {
@@ -494,14 +575,13 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 #pragma unroll
             for (int l = 0; l < NL; ++l) {
               const uint32_t u = unit + l * a.runs + m, buf = u % NU;
-              const float sw = sws[(l * 4 + (c - cs) * a.runs + m) * BM];
+              const float* from = sws + (l * 4 + (c - cs) * a.runs + m) * BM;
+              const float sw[4] = {from[0], from[8], from[16], from[24]};
               W4T_WAIT(tfull0 + 8u * buf, (u / NU) & 1u);
-              ok = __all_sync(0xffffffffu, ok);  // the loads below are the whole warp's
-              if (ok) {
-                tc_fence_after();
-                fold_run<COLS>(acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs);
-                tc_fence_before();
-              }
+              __syncwarp();  // the loads are the whole warp's, also after a wait that gave up
+              tc_fence_after();
+              fold_run<COLS>(acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs);
+              tc_fence_before();
               __syncwarp();
               if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
             }
@@ -511,30 +591,31 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(sempty0 + 8u * at);
       }
+      const int col_t = 2 * (lane & 3);
       if constexpr (C::BIG) {
-        const bool live = row < p.d_row;
-        const int64_t t1 = tok0 + half * COLS;
-        const int left = static_cast<int>(min(static_cast<int64_t>(COLS), p.n - t1));
-        const int64_t at = t1 * p.ldy + row;
+        const bool codes = NL == 2 && p.out == w4a8::OUT_I8;
         if (NL == 2) {
 #pragma unroll
           for (int j = 0; j < COLS / 2; ++j) {
-            const float2 g = unpack2(acc[0][j]), u = unpack2(acc[NL - 1][j]);
-            acc[0][j] = pack2(w4a8::silu_times(g.x, u.x), w4a8::silu_times(g.y, u.y));
+            const float2 g = unpack2(acc[0].v[j]), u = unpack2(acc[NL - 1].v[j]);
+            acc[0].v[j] = pack2(w4a8::silu_times(g.x, u.x), w4a8::silu_times(g.y, u.y));
           }
         }
-        if (NL == 2 && p.out == w4a8::OUT_I8) {
+        if (codes) {
           // maxima over the tile's 128 rows, through shared memory
 #pragma unroll
-          for (int j = 0; j < COLS / 2; ++j) {
-            const float2 h = unpack2(acc[0][j]);
-            const uint32_t m0 = __reduce_max_sync(0xffffffffu, live ? act8::abs_bits(h.x) : 0u);
-            const uint32_t m1 = __reduce_max_sync(0xffffffffu, live ? act8::abs_bits(h.y) : 0u);
-            if (lane == 0) {
-              tops[quarter * TN + half * COLS + 2 * j] = m0;
-              tops[quarter * TN + half * COLS + 2 * j + 1] = m1;
+          for (int q = 0; q < COLS / 8; ++q)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int hi = 0; hi < 4; ++hi)
+                if (row0 + row_t + 8 * hi < p.d_row)
+                  top = max(top, act8::abs_bits(acc[0].at(q >> 2, hi >> 1, q & 3, hi & 1, e2)));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              if (lane < 4) tops[quarter * TN + half * COLS + 8 * q + col_t + e2] = top;
             }
-          }
           named_bar(1, EW * 32);
           if (e < TN) {  // one thread a token: its scale, and what the rows multiply by
             const act8::Quant q = act8::quant_of(
@@ -544,24 +625,27 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (tok0 + e < p.n) p.ys[(tok0 + e) * ((p.d_row + 127) / 128) + row0 / BM] = q.scale;
           }
           named_bar(1, EW * 32);
-          int8_t* y = static_cast<int8_t*>(p.y) + at;
-#pragma unroll
-          for (int j = 0; j < COLS; ++j) {
-            act8::Quant q;
-            q.inv = __uint_as_float(tops[half * COLS + j]);
-            q.lift = __uint_as_float(tops[TN + half * COLS + j]);
-            const float2 h = unpack2(acc[0][j / 2]);
-            if (j < left && live)
-              y[j * p.ldy] = static_cast<int8_t>(act8::code_or_zero(j & 1 ? h.y : h.x, q));
-          }
-          named_bar(1, EW * 32);  // all have read before the next tile's maxima
-        } else if (live) {
-#pragma unroll
-          for (int j = 0; j < COLS; ++j) {
-            const float2 h = unpack2(acc[0][j / 2]);
-            if (j < left) w4a8::store_out(p, at + j * p.ldy, j & 1 ? h.y : h.x);
-          }
         }
+        // of each eight tokens the warp's lanes trade rows for (token, rows)
+        // pairs: lane j of eight gets token j % 2 of its two, rows 8 (j / 2) ..
+        const int j = (lane >> 2) & 7;
+        const int64_t row = row0 + quarter * 32 + 8 * (j >> 1);
+#pragma unroll
+        for (int q = 0; q < COLS / 8; ++q) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = acc[0].at(q >> 2, k >> 2, q & 3, (k >> 1) & 1, k & 1);
+          transpose8(v);
+          const int col = half * COLS + 8 * q + col_t + (j & 1);
+          act8::Quant k{};
+          if (codes) {
+            k.inv = __uint_as_float(tops[col]);
+            k.lift = __uint_as_float(tops[TN + col]);
+          }
+          if (tok0 + col < p.n)
+            store_rows8(p, (tok0 + col) * p.ldy + row, v, static_cast<int>(p.d_row - row), a.yvec, k);
+        }
+        if (codes) named_bar(1, EW * 32);  // all have read before the next tile's maxima
       } else {
         // the sums, token-major, over the ring: every copy has been consumed
         named_bar(1, EW * 32);
@@ -569,12 +653,13 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 #pragma unroll
         for (int l = 0; l < NL; ++l)
 #pragma unroll
-          for (int j = 0; j < COLS / 2; ++j) {
-            const float2 v = unpack2(acc[l][j]);
-            float* to = sums + (l * TN + half * COLS + 2 * j) * BM + quarter * 32 + lane;
-            to[0] = v.x;
-            to[BM] = v.y;
-          }
+          for (int q = 0; q < COLS / 8; ++q)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              float* to = sums + (l * TN + half * COLS + 8 * q + col_t + e2) * SUM_PITCH + row_t;
+#pragma unroll
+              for (int hi = 0; hi < 4; ++hi) to[8 * hi] = acc[l].at(q >> 2, hi >> 1, q & 3, hi & 1, e2);
+            }
       }
     }
   }
@@ -601,7 +686,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       float4 v[NL];
 #pragma unroll
       for (int l = 0; l < NL; ++l) {
-        float* own = sums + (l * TN + tk) * BM + 4 * lane;
+        float* own = sums + (l * TN + tk) * SUM_PITCH + 4 * lane;
         v[l] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int r = 0; r < a.ksplit; ++r) {
           const float4 o = *reinterpret_cast<const float4*>(cl.map_shared_rank(own, r));
