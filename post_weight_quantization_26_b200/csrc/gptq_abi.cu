@@ -91,9 +91,9 @@ struct DeviceInfo {
 template <bool GATED>
 struct W4a8Cfg {
   static constexpr int NL = GATED ? 2 : 1;
-  using Small = w4a8t::Cfg<NL, 64 / NL, 4, 8 / NL, GATED ? 3 : 4, 2, GATED ? 1 : 2, false>;
-  using Mid = w4a8t::Cfg<NL, 128 / NL, 4, 8, 5, GATED ? 4 : 3, 1, false>;
-  using Big = w4a8t::Cfg<NL, 256 / NL, 8, 16, 4, GATED ? 4 : 3, 1, true>;
+  using Small = w4a8t::Cfg<NL, 64 / NL, 8, 8 / NL, GATED ? 3 : 4, 4, 3, GATED ? 152 : 104, false>;
+  using Mid = w4a8t::Cfg<NL, 128 / NL, 4, 8, 3, 4, 2, 168, false>;
+  using Big = w4a8t::Cfg<NL, 256 / NL, 8, 16, 2, GATED ? 4 : 3, 2, 96, true>;
 };
 
 // The shared memory of a kernel, and the carveout that lets several of its
@@ -702,9 +702,9 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   if (!C::BIG) {
     // The split that ends first: rounds of CTAs, each its chunks and a ramp
     // worth about six chunks (launch, first loads, the sums' exchange).
-    const int64_t slots = static_cast<int64_t>(num_sms) * C::MINB;
+    const int64_t slots = static_cast<int64_t>(num_sms);
     int64_t best = INT64_MAX;
-    for (int k = 1; k <= 8 && k <= nchunks; k *= 2) {
+    for (int k = 1; k <= 8 && k <= (nchunks + 3) / 4; k *= 2) {
       const int64_t cost = ((tiles * k + slots - 1) / slots) * ((nchunks + k - 1) / k + 6);
       if (cost < best) { best = cost; a.ksplit = k; }
     }
@@ -712,7 +712,7 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   CUtensorMap mw[2], mx;
   for (int l = 0; l < 2; ++l) {
     gptq_status st = encode_u8_2d(&mw[l], p.layer[l < C::NL ? l : 0].qweight, p.d_col / 2, p.d_row,
-                                  p.d_col / 2, w4a8t::CH / 2, w4a8t::BM, CU_TENSOR_MAP_SWIZZLE_64B);
+                                  p.d_col / 2, w4a8t::CH, w4a8t::BM, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != GPTQ_OK) return st;
   }
   gptq_status st = encode_u8_2d(&mx, p.x, p.d_col, p.n, p.ldx, w4a8t::CH, C::TN,

@@ -41,41 +41,42 @@ using w4a8::Params;
 
 constexpr int BM = 128;  // layer rows per tile
 constexpr int CH = 128;  // columns per chunk
-constexpr int PACKED_BYTES = BM * CH / 2;
+constexpr int PACKED_BYTES = BM * CH;  // a stage's words: two chunks, 128 bytes a row
 constexpr int SLOT_BYTES = BM * CH;
 constexpr int SUM_PITCH = BM + 4;  // rows of a token's sums: spreads a warp's 8 rows x 4 tokens
 
 // NL: layers; TN: tokens per tile; UW, EW: unpack and epilogue warps; S: ring
-// stages; AS: operand slots of one layer and chunk; MINB: CTAs per SM.  Four
+// stages; AS: operand slots of one layer and chunk; NS: sets of scales on the
+// way or in use; MORE: registers of an epilogue thread.  Four
 // more warps are the TMA warp, the MMA warp and two that fetch scales.
-template <int NL_, int TN_, int UW_, int EW_, int S_, int AS_, int MINB_, bool BIG_>
+template <int NL_, int TN_, int UW_, int EW_, int S_, int AS_, int NS_, int MORE_, bool BIG_>
 struct Cfg {
-  static constexpr int NL = NL_, TN = TN_, UW = UW_, EW = EW_, S = S_, AS = AS_, MINB = MINB_;
+  static constexpr int NL = NL_, TN = TN_, UW = UW_, EW = EW_, S = S_, AS = AS_, NS = NS_;
   static constexpr bool BIG = BIG_;
   static constexpr int WARPS = UW + EW + 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int NU = 512 / MINB / TN < 4 ? 512 / MINB / TN : 4;  // TMEM buffers
+  static constexpr int NU = 512 / TN < 4 ? 512 / TN : 4;  // TMEM buffers
   static constexpr int TMEM_COLS = NU * TN < 32 ? 32 : NU * TN;
   static constexpr int COLS = TN / (EW / 4);         // columns (tokens) per epilogue warp
   static constexpr int X_BYTES = TN * CH;
-  static constexpr int STAGE_BYTES = NL * PACKED_BYTES + X_BYTES;
+  static constexpr int STAGE_BYTES = NL * PACKED_BYTES + 2 * X_BYTES;
   static constexpr int RING_BYTES = S * STAGE_BYTES;
   static constexpr int SUM_BYTES = BIG ? 0 : NL * TN * SUM_PITCH * 4;  // over the ring, at the end
-  static constexpr int SX_BYTES = 2 * 4 * TN * 4;       // two sets of token scales
-  static constexpr int SW_BYTES = 2 * 4 * NL * BM * 4;  // two sets of row scales
-  static constexpr int Z_BYTES = 2 * NL * BM * 4;       // and of zero points, four in a word
-  static constexpr int TOP_BYTES = BIG ? 4 * TN * 4 : 0;
-  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 5;
+  static constexpr int SX_BYTES = NS * 4 * TN * 4;       // sets of token scales, four a token
+  static constexpr int SW_BYTES = NS * 4 * NL * BM * 4;  // of row scales, four a row
+  static constexpr int Z_BYTES = NS * NL * BM * 4;       // of zero points, four in a word
+  static constexpr int TOP_BYTES = BIG && NL == 2 ? 4 * TN * 4 : 0;
+  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 2 * NS + 1;
   static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + Z_BYTES + TOP_BYTES +
                               BARS * 8 + 16 + 1024 /* alignment */;
   static_assert(NU >= NL && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
-  static_assert(EW % 4 == 0 && UW % 4 == 0 && COLS % 32 == 0, "warps");
-  static_assert((SMEM + 1024) * MINB <= 228 * 1024, "shared memory");
-  // BIG moves registers between warpgroups: the launch's are THREADS x LAUNCH
-  static constexpr int LAUNCH = 65536 / THREADS / 8 * 8, MORE = 96,
+  static_assert(EW % 4 == 0 && UW % 4 == 0 && (COLS == 32 || COLS == 64), "warps");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  // the launch's registers, THREADS x LAUNCH, move between warpgroups
+  static constexpr int LAUNCH = 65536 / THREADS / 8 * 8, MORE = MORE_,
                        FEWER = (THREADS * LAUNCH - EW * 32 * MORE) / ((UW + 4) * 32) / 8 * 8;
-  static_assert(!BIG || (EW * MORE + (UW + 4) * FEWER) * 32 <= THREADS * LAUNCH, "registers");
+  static_assert((EW * MORE + (UW + 4) * FEWER) * 32 <= THREADS * LAUNCH && FEWER >= 40, "registers");
 };
 
 struct Tiled {
@@ -104,6 +105,15 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+
+// 4 or 16 bytes into shared memory without passing through a register.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
 // Four signed bytes q - z of one word's even or odd codes, still biased by 128.
@@ -139,9 +149,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 16 lanes x 32 columns of TMEM: register 4 b + 2 i + e of lane t has row
-// t / 4 + 8 i, column 8 b + 2 (t % 4) + e.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 lanes x 32 columns of TMEM: register 4 b + 2 i + e of lane t has
+// row t / 4 + 8 i, column 8 b + 2 (t % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -153,16 +163,15 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 }
 
 // A thread's share of 32 rows x COLS tokens: rows lane / 4 + 8 i + 16 h, and
-// of each eight tokens two.  acc[((p 2 + h) 4 + b) 2 + i] has the tokens
-// 32 p + 8 b + 2 (lane % 4) + {0, 1} of row (h, i).  With four rows a thread
-// needs a quarter of the tokens' scales: one row a thread and all tokens read
-// 128 B a warp and value from shared memory, 620 clocks a chunk of 128 x 256
-// outputs.
+// of each eight tokens two: v[(h COLS / 8 + b) 2 + i] has the tokens 8 b +
+// 2 (lane % 4) + {0, 1} of row (h, i).  With four rows a thread needs a quarter
+// of the tokens' scales: one row a thread and all tokens read 128 B a warp and
+// value from shared memory, 620 clocks a chunk of 128 x 256 outputs.
 template <int COLS>
 struct Share {
   uint64_t v[COLS / 2];
-  __device__ __forceinline__ float at(int p, int h, int b, int i, int e) const {
-    const float2 f = unpack2(v[((p * 2 + h) * 4 + b) * 2 + i]);
+  __device__ __forceinline__ float at(int b, int h, int i, int e) const {
+    const float2 f = unpack2(v[(h * (COLS / 8) + b) * 2 + i]);
     return e ? f.y : f.x;
   }
 };
@@ -210,43 +219,60 @@ __device__ __forceinline__ void store_rows8(const Params& p, int64_t at, const f
 }
 
 // One run's sums, scaled and added; t0: the warp's lanes and first column in
-// TMEM, sw: its four rows' scales, sx: the first token's scale.  The conversion
-// to fp32 is an instruction of half the adders' rate; the add of 1.5 * 2^23
-// and its subtraction would cost as much and more issue slots.
+// TMEM, sw: its four rows' scales, sx: the first token's scale.  The reads of
+// TMEM are issued 32 columns and 16 lanes at a time, or all before the first is
+// used where the registers are there (ALL).  The conversion to fp32 is an
+// instruction of half the adders' rate; the add of 1.5 * 2^23 and its
+// subtraction would cost as much and more issue slots.
 template <int COLS>
+__device__ __forceinline__ void fold_32(Share<COLS>& acc, const uint32_t (&v)[16], int p, int h,
+                                        const float (&sw)[4], const uint64_t (&s)[4]) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t f = pack2(__int2float_rn(static_cast<int>(v[4 * b + 2 * i])),
+                               __int2float_rn(static_cast<int>(v[4 * b + 2 * i + 1])));
+      uint64_t& a = acc.v[(h * (COLS / 8) + 4 * p + b) * 2 + i];
+      a = fma2(f, mul2(pack2(sw[2 * h + i], sw[2 * h + i]), s[b]), a);
+    }
+}
+template <int COLS, bool ALL>
 __device__ __forceinline__ void fold_run(Share<COLS>& acc, uint32_t t0, const float (&sw)[4],
                                          const float* sx) {
-  const float* sxt = sx + 2 * (threadIdx.x & 3);
+  const float* sxt = sx + 8 * (threadIdx.x & 3);  // four a token
+  constexpr int P = COLS / 32;
+  uint32_t v[ALL ? P : 1][ALL ? 2 : 1][16];
+  if (ALL) {
 #pragma unroll
-  for (int p = 0; p < COLS / 32; ++p) {
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        tmem_ld_16x256b(t0 + (static_cast<uint32_t>(16 * h) << 16) + 32 * p, v[p][h]);
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
     uint64_t s[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t v[16];
-      tmem_ld_16x256b_x4(t0 + (static_cast<uint32_t>(16 * h) << 16) + 32 * p, v);
+      if (!ALL) tmem_ld_16x256b(t0 + (static_cast<uint32_t>(16 * h) << 16) + 32 * p, v[0][0]);
       if (h == 0)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) s[b] = *reinterpret_cast<const uint64_t*>(sxt + 32 * p + 8 * b);
-      tmem_ld_wait();
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint64_t f = pack2(__int2float_rn(static_cast<int>(v[4 * b + 2 * i])),
-                                   __int2float_rn(static_cast<int>(v[4 * b + 2 * i + 1])));
-          uint64_t& a = acc.v[((p * 2 + h) * 4 + b) * 2 + i];
-          a = fma2(f, mul2(pack2(sw[2 * h + i], sw[2 * h + i]), s[b]), a);
-        }
+        for (int b = 0; b < 4; ++b)
+          s[b] = pack2(sxt[4 * (32 * p + 8 * b)], sxt[4 * (32 * p + 8 * b) + 4]);
+      if (!ALL || (p == 0 && h == 0)) tmem_ld_wait();
+      fold_32<COLS>(acc, v[ALL ? p : 0][ALL ? h : 0], p, h, sw, s);
     }
   }
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::MINB)
+__global__ void __launch_bounds__(C::THREADS, 1)
 w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                   const __grid_constant__ CUtensorMap tmap_w1,
                   const __grid_constant__ CUtensorMap tmap_x, const Tiled a) {
-  constexpr int NL = C::NL, TN = C::TN, S = C::S, AS = C::AS, NU = C::NU, EW = C::EW, UW = C::UW;
+  constexpr int NL = C::NL, TN = C::TN, S = C::S, AS = C::AS, NU = C::NU, NS = C::NS, EW = C::EW,
+                UW = C::UW;
   constexpr uint32_t IDESC = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(TN >> 3) << 17) |
                              (uint32_t(BM >> 4) << 24);  // s32 += s8 x s8, both K-major
   namespace cg = cooperative_groups;
@@ -265,26 +291,26 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, afull0 = empty0 + 8u * S,
                  aempty0 = afull0 + 8u * AS, tfull0 = aempty0 + 8u * AS,
-                 tempty0 = tfull0 + 8u * NU, sfull0 = tempty0 + 8u * NU, sempty0 = sfull0 + 16u,
-                 drain = sempty0 + 16u;
+                 tempty0 = tfull0 + 8u * NU, sfull0 = tempty0 + 8u * NU, sempty0 = sfull0 + 8u * C::NS,
+                 drain = sempty0 + 8u * C::NS;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool leader = elect_one();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, 1);
-      mbar_init(empty0 + 8u * s, UW + 1);  // unpacked, and multiplied
+      mbar_init(empty0 + 8u * s, 8 * NL + 1);  // unpacked, and multiplied
     }
     for (int s = 0; s < AS; ++s) {
-      mbar_init(afull0 + 8u * s, UW);
+      mbar_init(afull0 + 8u * s, 4);
       mbar_init(aempty0 + 8u * s, 1);
     }
     for (int u = 0; u < NU; ++u) {
       mbar_init(tfull0 + 8u * u, 1);
       mbar_init(tempty0 + 8u * u, EW);
     }
-    for (int u = 0; u < 2; ++u) {
-      mbar_init(sfull0 + 8u * u, 2);
+    for (int u = 0; u < C::NS; ++u) {
+      mbar_init(sfull0 + 8u * u, 64);  // the scale warps' lanes
       mbar_init(sempty0 + 8u * u, UW + EW);
     }
     mbar_init(drain, 1);
@@ -305,8 +331,11 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 
   const int nchunks = (p.d_col + CH - 1) / CH;
   const int krank = C::BIG ? 0 : static_cast<int>(blockIdx.x) % a.ksplit;
-  const int c0 = static_cast<int>(static_cast<int64_t>(nchunks) * krank / a.ksplit);
-  const int c1 = static_cast<int>(static_cast<int64_t>(nchunks) * (krank + 1) / a.ksplit);
+  // shares of whole fours of chunks, so that sets of scales start aligned
+  const int quads = (nchunks + 3) / 4;
+  const int c0 = 4 * (quads * krank / a.ksplit);
+  // an odd last chunk makes a pair with one of zeros, which the copies fill in
+  const int c1 = min((nchunks + 1) / 2 * 2, 4 * (quads * (krank + 1) / a.ksplit));
   const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.tok_tiles;
   const int64_t tile0 = C::BIG ? blockIdx.x : blockIdx.x / a.ksplit;
   const int64_t tile_step = C::BIG ? gridDim.x : tiles;
@@ -323,9 +352,9 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   (ok = ok && mbar_wait_bounded((bar), (par), abort_flag, a.wait_ns))
 
 #define W4T_FEWER() \
-  if (C::BIG) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEWER))
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEWER))
 #define W4T_MORE() \
-  if (C::BIG) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE))
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MORE))
 
   if (warp >= UW + EW) {
     W4T_FEWER();  // the whole warpgroup, at one place
@@ -336,7 +365,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
         const int row = static_cast<int>(t / a.tok_tiles) * BM;
         const int tok = static_cast<int>(t % a.tok_tiles) * TN;
-        for (int c = c0; c < c1; ++c) {
+        for (int c = c0; c < c1; c += 2) {
           if (!W4T_WAIT(empty0 + 8u * st, ph ^ 1u)) break;
           const uint32_t fb = full0 + 8u * st, at = ring + st * C::STAGE_BYTES;
           if (leader) {
@@ -344,6 +373,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             tma_load_2d(at, &tmap_w0, fb, c * (CH / 2), row);
             if (NL == 2) tma_load_2d(at + PACKED_BYTES, &tmap_w1, fb, c * (CH / 2), row);
             tma_load_2d(at + NL * PACKED_BYTES, &tmap_x, fb, c * CH, tok);
+            tma_load_2d(at + NL * PACKED_BYTES + C::X_BYTES, &tmap_x, fb, (c + 1) * CH, tok);
             ++issued;
           }
           __syncwarp();
@@ -360,13 +390,17 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     } else if (warp == UW + EW + 1) {
       // ------------------------------------------------------------ MMA warp
       const uint64_t DESC = smem_desc_sw128(0, 16, 1024);  // addresses are added
-      uint32_t st = 0, ph = 0, slot = 0, sph = 0, unit = 0;
+      uint32_t st = 0, slot = 0, sph = 0, unit = 0;
       bool open = false;  // the current buffers hold a started run
       for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
         for (int c = c0; c < c1 && ok; ++c) {
           const bool close = closes(c);
-          if (!W4T_WAIT(full0 + 8u * st, ph)) break;
-          const uint64_t xd = DESC + ((ring + st * C::STAGE_BYTES + NL * PACKED_BYTES) >> 4);
+          // The tokens' codes came with the words that the unpack warps waited
+          // for, so their arrival stands for both: a wait costs this warp 170
+          // clocks even where there is nothing to wait for, a third of what a
+          // chunk may take.
+          const uint64_t xd = DESC + ((ring + st * C::STAGE_BYTES + NL * PACKED_BYTES +
+                                       (c & 1) * C::X_BYTES) >> 4);
 #pragma unroll
           for (int l = 0; l < NL; ++l) {
             const uint64_t ad = DESC + ((slots + slot * SLOT_BYTES) >> 4);
@@ -401,9 +435,11 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (ok && leader) mma_commit(aempty0 + 8u * slot);
             if (++slot == AS) { slot = 0; sph ^= 1u; }
           }
-          if (ok && leader) mma_commit(empty0 + 8u * st);
+          if (c & 1) {
+            if (ok && leader) mma_commit(empty0 + 8u * st);
+            if (++st == S) st = 0;
+          }
           __syncwarp();
-          if (++st == S) { st = 0; ph ^= 1u; }
           open = !close;
           if (close) unit += NL * a.runs;
         }
@@ -416,91 +452,82 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     } else {
       // --------------------------------------------------------- scale warps
       // The scales and zero points of the next runs, in sets of four runs (4,
-      // 2 or 1 chunks), and those chunks' token scales.  A lane reads a row's
-      // or token's four at once where they lie in 16 aligned bytes: one value
-      // at a time, 32 lines a load, the reads took more of the load unit than
-      // all else in the kernel (640 clocks a chunk of 128 x 256 outputs).
+      // 2 or 1 chunks), and those chunks' token scales: a lane copies a row's
+      // or token's four at once where they lie in 16 aligned bytes, straight
+      // to shared memory and NS sets ahead, as row scales come from HBM.  (One
+      // value at a time and line took more of the load unit than all else, 640
+      // clocks a chunk of 128 x 256 outputs.)
       const int i = threadIdx.x - (UW + EW + 2) * 32;  // 0..63
       const int per_set = 4 / a.runs, step = CH / a.runs;
-      constexpr int TK = (TN + 63) / 64;  // tokens of a thread
       uint32_t set = 0;
       for (int64_t t = tile0; t < tiles; t += tile_step) {
         const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
         const int64_t tok0 = (t % a.tok_tiles) * TN;
         for (int cs = c0; cs < c1; cs += per_set, ++set) {
-          const uint32_t at = set & 1u;
-          float4 x[TK];
+          const uint32_t at = set % NS;
+          const int g[4] = {group_of(cs * CH), group_of(cs * CH + step), group_of(cs * CH + 2 * step),
+                            group_of(cs * CH + 3 * step)};
           const bool xvec = a.xvec && (cs & 3) == 0 && cs + 4 <= p.xgroups;
+          const bool wvec = a.wvec && (g[0] & 3) == 0 && g[3] == g[0] + 3;
+          W4T_WAIT(sempty0 + 8u * at, ((set / NS) & 1u) ^ 1u);
+          if (ok) {
+            for (int r = i; r < TN; r += 64) {
+              const float* from = p.xs + min(tok0 + r, p.n - 1) * p.xgroups;
+              float* to = sx + (at * TN + r) * 4;
+              if (xvec) {
+                copy_async<16>(to, from + cs);
+              } else {
 #pragma unroll
-          for (int k = 0; k < TK; ++k) {
-            const float* from = p.xs + min(tok0 + i + 64 * k, p.n - 1) * p.xgroups;
-            if (xvec) {
-              x[k] = __ldg(reinterpret_cast<const float4*>(from + cs));
-            } else if (p.xgroups == 1) {
-              x[k].x = x[k].y = x[k].z = x[k].w = __ldg(from);
+                for (int j = 0; j < 4; ++j)
+                  copy_async<4>(to + j, from + (p.xgroups == 1 ? 0 : min(cs + j, nchunks - 1)));
+              }
+            }
+#pragma unroll
+            for (int l = 0; l < NL; ++l)
+              for (int r = i; r < BM; r += 64) {
+                const size_t first = static_cast<size_t>(min(row0 + r, p.d_row - 1)) * p.n_groups;
+                const float* sf = p.layer[l].scales + first;
+                const uint8_t* zf = p.layer[l].zeros + first;
+                float* to = swb + ((at * NL + l) * BM + r) * 4;
+                uint32_t* zt = zb + (at * NL + l) * BM + r;
+                if (wvec) {
+                  copy_async<16>(to, sf + g[0]);
+                  copy_async<4>(zt, zf + g[0]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) copy_async<4>(to + j, sf + g[j]);
+                  *zt = __ldg(zf + g[0]) | (__ldg(zf + g[1]) << 8) | (__ldg(zf + g[2]) << 16) |
+                        (static_cast<uint32_t>(__ldg(zf + g[3])) << 24);
+                }
+              }
+            if (wvec) {  // the copies' own arrival, when they are done
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8u * at)
+                           : "memory");
             } else {
-              x[k].x = __ldg(from + cs);
-              x[k].y = __ldg(from + min(cs + 1, nchunks - 1));
-              x[k].z = __ldg(from + min(cs + 2, nchunks - 1));
-              x[k].w = __ldg(from + min(cs + 3, nchunks - 1));
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              mbar_arrive(sfull0 + 8u * at);
             }
           }
-          const int g0 = group_of(cs * CH), g1 = group_of(cs * CH + step),
-                    g2 = group_of(cs * CH + 2 * step), g3 = group_of(cs * CH + 3 * step);
-          const bool wvec = a.wvec && (g0 & 3) == 0 && g3 == g0 + 3;
-          W4T_WAIT(sempty0 + 8u * at, ((set >> 1) & 1u) ^ 1u);
-#pragma unroll
-          for (int l = 0; l < NL; ++l)
-#pragma unroll
-            for (int k = 0; k < BM / 64; ++k) {
-              const int r = i + 64 * k;
-              const size_t first = static_cast<size_t>(min(row0 + r, p.d_row - 1)) * p.n_groups;
-              const float* sf = p.layer[l].scales + first;
-              const uint8_t* zf = p.layer[l].zeros + first;
-              float4 v;
-              uint32_t z;
-              if (wvec) {
-                v = __ldg(reinterpret_cast<const float4*>(sf + g0));
-                z = __ldg(reinterpret_cast<const uint32_t*>(zf + g0));
-              } else {
-                v = make_float4(__ldg(sf + g0), __ldg(sf + g1), __ldg(sf + g2), __ldg(sf + g3));
-                z = __ldg(zf + g0) | (__ldg(zf + g1) << 8) | (__ldg(zf + g2) << 16) |
-                    (static_cast<uint32_t>(__ldg(zf + g3)) << 24);
-              }
-              float* wo = swb + (at * NL + l) * 4 * BM + r;
-              wo[0] = v.x;
-              wo[BM] = v.y;
-              wo[2 * BM] = v.z;
-              wo[3 * BM] = v.w;
-              zb[(at * NL + l) * BM + r] = z;
-            }
-          float* xo = sx + at * 4 * TN + i;
-#pragma unroll
-          for (int k = 0; k < TK; ++k)
-            if (TN % 64 == 0 || i + 64 * k < TN) {
-              xo[64 * k] = x[k].x;
-              xo[TN + 64 * k] = x[k].y;
-              xo[2 * TN + 64 * k] = x[k].z;
-              xo[3 * TN + 64 * k] = x[k].w;
-            }
-          __syncwarp();
-          if (ok && lane == 0) mbar_arrive(sfull0 + 8u * at);
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else if (warp < UW) {
     // -------------------------------------------------------------- unpack
     W4T_FEWER();
+    // Groups of four warps take the operand slots (a chunk of one layer) in
+    // turn: a slot's way from barrier to barrier is a chain of latencies, and
+    // one group at it was the pace of the whole kernel.
+    constexpr uint32_t UG = UW / 4;
+    const uint32_t group = warp >> 2;
     const int r = threadIdx.x & (BM - 1);  // row of the tile
-    constexpr int PIECES = 16 / UW;        // 16-byte pieces (32 codes) of a thread
-    const int i0 = (threadIdx.x / BM) * PIECES;
-    const uint32_t in_row = r * 64, out_row = r * 128;
-    uint32_t st = 0, ph = 0, slot = 0, sph = 0, set = 0;
+    const uint32_t in_row = r * 128, out_row = r * 128;
+    uint32_t k = 0, kc = 0, set = 0;  // slots, chunks and sets so far
     const int per_set = 4 / a.runs;
     for (int64_t t = tile0; t < tiles; t += tile_step) {
       for (int cs = c0; cs < c1; cs += per_set, ++set) {
-        const uint32_t at = set & 1u;
-        W4T_WAIT(sfull0 + 8u * at, (set >> 1) & 1u);
+        const uint32_t at = set % NS;
+        W4T_WAIT(sfull0 + 8u * at, (set / NS) & 1u);
         uint32_t z[NL];  // four zero points of the row
 #pragma unroll
         for (int l = 0; l < NL; ++l) z[l] = zb[(at * NL + l) * BM + r];
@@ -508,38 +535,40 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
         if (ok && lane == 0) mbar_arrive(sempty0 + 8u * at);
         const int ce = min(cs + per_set, c1);
 #pragma unroll 1
-        for (int c = cs; c < ce; ++c) {
-          W4T_WAIT(full0 + 8u * st, ph);
-          const uint8_t* in = base + st * C::STAGE_BYTES + in_row;
+        for (int c = cs; c < ce; ++c, ++kc) {
+          const uint32_t st = (kc >> 1) % S;
 #pragma unroll
-          for (int l = 0; l < NL; ++l) {
+          for (int l = 0; l < NL; ++l, ++k) {
+            if (k % UG != group) continue;
+            const uint32_t slot = k % AS;
+            W4T_WAIT(full0 + 8u * st, ((kc >> 1) / S) & 1u);
+            const uint8_t* in = base + st * C::STAGE_BYTES + l * PACKED_BYTES + in_row;
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = *reinterpret_cast<const uint4*>(in + (((4 * (c & 1) + i) ^ (r & 7)) << 4));
             const uint32_t first = (c - cs) * a.runs;  // the chunk's first run in the set
-            uint4 w[PIECES];
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i)
-              w[i] = *reinterpret_cast<const uint4*>(in + l * PACKED_BYTES +
-                                                     (((i0 + i) ^ ((r >> 1) & 3)) << 4));
-            W4T_WAIT(aempty0 + 8u * slot, sph ^ 1u);
+            W4T_WAIT(aempty0 + 8u * slot, ((k / AS) & 1u) ^ 1u);
             uint8_t* out = base + C::RING_BYTES + slot * SLOT_BYTES + out_row;
             if (ok) {
 #pragma unroll
-              for (int i = 0; i < PIECES; ++i) {
-                const uint32_t zi = __byte_perm(z[l], 0, (first + ((i0 + i) * a.runs >> 2)) * 0x1111);
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t zi = __byte_perm(z[l], 0, (first + (i * a.runs >> 2)) * 0x1111);
                 const uint2 b0 = unpack_word(w[i].x, zi), b1 = unpack_word(w[i].y, zi);
                 const uint2 b2 = unpack_word(w[i].z, zi), b3 = unpack_word(w[i].w, zi);
-                *reinterpret_cast<uint4*>(out + (((2 * (i0 + i)) ^ (r & 7)) << 4)) =
+                *reinterpret_cast<uint4*>(out + (((2 * i) ^ (r & 7)) << 4)) =
                     make_uint4(b0.x, b0.y, b1.x, b1.y);
-                *reinterpret_cast<uint4*>(out + (((2 * (i0 + i) + 1) ^ (r & 7)) << 4)) =
+                *reinterpret_cast<uint4*>(out + (((2 * i + 1) ^ (r & 7)) << 4)) =
                     make_uint4(b2.x, b2.y, b3.x, b3.y);
               }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(afull0 + 8u * slot);
-            if (++slot == AS) { slot = 0; sph ^= 1u; }
+            if (ok && lane == 0) {
+              mbar_arrive(afull0 + 8u * slot);
+              mbar_arrive(empty0 + 8u * st);
+            }
           }
-          if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
-          if (++st == S) { st = 0; ph ^= 1u; }
         }
       }
     }
@@ -562,25 +591,25 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 #pragma unroll
         for (int j = 0; j < COLS / 2; ++j) acc[l].v[j] = 0ull;
       for (int cs = c0; cs < c1; cs += per_set, ++set) {
-        const uint32_t at = set & 1u;
-        W4T_WAIT(sfull0 + 8u * at, (set >> 1) & 1u);
-        const float* sxs = sx + at * 4 * TN + half * COLS;
-        const float* sws = swb + at * NL * 4 * BM + row_t;
+        const uint32_t at = set % NS;
+        W4T_WAIT(sfull0 + 8u * at, (set / NS) & 1u);
+        const float* sxs = sx + (at * TN + half * COLS) * 4;
+        const float* sws = swb + (at * NL * BM + row_t) * 4;
         const int ce = min(cs + per_set, c1);
 #pragma unroll 1
-        for (int c = cs; c < ce; ++c, sxs += TN) {
+        for (int c = cs; c < ce; ++c, ++sxs) {
           if (!closes(c)) continue;
 #pragma unroll 1
           for (int m = 0; m < a.runs; ++m) {
 #pragma unroll
             for (int l = 0; l < NL; ++l) {
               const uint32_t u = unit + l * a.runs + m, buf = u % NU;
-              const float* from = sws + (l * 4 + (c - cs) * a.runs + m) * BM;
-              const float sw[4] = {from[0], from[8], from[16], from[24]};
+              const float* from = sws + l * BM * 4 + (c - cs) * a.runs + m;
+              const float sw[4] = {from[0], from[32], from[64], from[96]};  // rows + 8 i + 16 h
               W4T_WAIT(tfull0 + 8u * buf, (u / NU) & 1u);
               __syncwarp();  // the loads are the whole warp's, also after a wait that gave up
               tc_fence_after();
-              fold_run<COLS>(acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs);
+              fold_run<COLS, (C::MORE >= 128)>(acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs);
               tc_fence_before();
               __syncwarp();
               if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
@@ -611,7 +640,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 #pragma unroll
               for (int hi = 0; hi < 4; ++hi)
                 if (row0 + row_t + 8 * hi < p.d_row)
-                  top = max(top, act8::abs_bits(acc[0].at(q >> 2, hi >> 1, q & 3, hi & 1, e2)));
+                  top = max(top, act8::abs_bits(acc[0].at(q, hi >> 1, hi & 1, e2)));
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
               if (lane < 4) tops[quarter * TN + half * COLS + 8 * q + col_t + e2] = top;
@@ -634,7 +663,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
         for (int q = 0; q < COLS / 8; ++q) {
           float v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = acc[0].at(q >> 2, k >> 2, q & 3, (k >> 1) & 1, k & 1);
+          for (int k = 0; k < 8; ++k) v[k] = acc[0].at(q, k >> 2, (k >> 1) & 1, k & 1);
           transpose8(v);
           const int col = half * COLS + 8 * q + col_t + (j & 1);
           act8::Quant k{};
@@ -658,7 +687,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             for (int e2 = 0; e2 < 2; ++e2) {
               float* to = sums + (l * TN + half * COLS + 8 * q + col_t + e2) * SUM_PITCH + row_t;
 #pragma unroll
-              for (int hi = 0; hi < 4; ++hi) to[8 * hi] = acc[l].at(q >> 2, hi >> 1, q & 3, hi & 1, e2);
+              for (int hi = 0; hi < 4; ++hi) to[8 * hi] = acc[l].at(q, hi >> 1, hi & 1, e2);
             }
       }
     }
