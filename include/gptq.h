@@ -346,6 +346,10 @@ gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const
                              const int8_t* codes, int64_t ldq, const float* x_scales, int x_group,
                              int64_t n, void* Y, int y_type, int64_t ldy, void* stream);
 
+/* Bytes of workspace that gptq_w4a8_gated needs for n tokens: rows of fp32 for
+ * an 8-bit output of at most 16 tokens, else 0 (then ws may be NULL). */
+size_t gptq_w4a8_workspace_size(int64_t n, int64_t d_row, int h_type);
+
 /* The gated pair of projections of a feed-forward block in one kernel, on two
  * packed 4-bit layers of the same shape and configuration:
  *   H = silu(X Wg^T) * (X Wu^T),   silu(v) = v / (1 + exp(-v)),
@@ -354,13 +358,18 @@ gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const
  *             x_group 128, which gptq_w4a8_matmul of the down projection
  *             reads; codes to H, scales to h_scales (fp32 n x ceil(d_row /
  *             128)).  h_scales is used for GPTQ_I8 only.
+ *  ws         >= gptq_w4a8_workspace_size(n, d_row, h_type) bytes (device,
+ *             256-byte aligned), else GPTQ_ERR_WORKSPACE.  With at most 16
+ *             tokens an 8-bit output is written by a second, small kernel;
+ *             calls that may overlap need a workspace each.
  *  Other arguments, limits and errors as gptq_w4a8_matmul. */
 gptq_status gptq_w4a8_gated(const uint32_t* qweight_gate, const float* scales_gate,
                             const uint8_t* zeros_gate, const uint32_t* qweight_up,
                             const float* scales_up, const uint8_t* zeros_up, int64_t d_row,
                             int64_t d_col, const gptq_config* cfg, const int8_t* codes,
                             int64_t ldq, const float* x_scales, int x_group, int64_t n, void* H,
-                            int h_type, int64_t ldh, float* h_scales, void* stream);
+                            int h_type, int64_t ldh, float* h_scales, void* ws, size_t ws_bytes,
+                            void* stream);
 
 /* AWQ channel scale (dingiv.github.io "量化" page, section AWQ: salient
  * input channels are found by their mean activation magnitude):

@@ -627,49 +627,48 @@ gptq_status w4a8_rows_launch(const w4a8::Params& p, int num_sms, cudaStream_t s)
   }
   if (st != GPTQ_OK) return st;
   cudaLaunchConfig_t lc{};
-  cudaLaunchAttribute at[1];
-  // whole clusters' worth of tiles for an 8-bit output
-  const unsigned step = p.out == GPTQ_I8 ? C::CLUSTER : 1;
-  const unsigned tiles =
-      (static_cast<unsigned>((p.d_row + C::ROWS - 1) / C::ROWS) + step - 1) / step * step;
-  a.tiles = static_cast<int>(tiles);
+  a.tiles = (p.d_row + C::ROWS - 1) / C::ROWS;
   lc.blockDim = dim3(w4a8::THREADS);
   lc.dynamicSmemBytes = C::SMEM;
   lc.stream = s;
-  if (p.out == GPTQ_I8) {
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C::CLUSTER;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-  }
-  // As many CTAs as are on the GPU at once (clusters: fewer than the SMs' room,
-  // as one lies within a GPC; a cluster that has to wait would double the
-  // time), and no more than it takes for the same number of rounds.
-  unsigned most = static_cast<unsigned>(num_sms) * C::MINB;
-  if (step > 1) {
-    static std::atomic<int> resident[64];
-    int dev = 0;
-    GPTQ_CUDA_TRY(cudaGetDevice(&dev));
-    int k = resident[dev].load();
-    if (k == 0) {
-      lc.gridDim = dim3(step);
-      GPTQ_CUDA_TRY(cudaOccupancyMaxActiveClusters(&k, w4a8::w4a8_rows_kernel<C>, &lc));
-      if (k < 1) return GPTQ_ERR_CUDA;
-      resident[dev].store(k);
-    }
-    most = static_cast<unsigned>(k) * step;
-  }
-  const unsigned rounds = (tiles + most - 1) / most;
-  lc.gridDim = dim3((tiles / step + rounds - 1) / rounds * step);
+  // as many CTAs as are on the GPU at once, and no more than it takes for the
+  // same number of rounds
+  const int most = num_sms * C::MINB, rounds = (a.tiles + most - 1) / most;
+  lc.gridDim = dim3(static_cast<unsigned>((a.tiles + rounds - 1) / rounds));
   cudaError_t e = cudaLaunchKernelEx(&lc, w4a8::w4a8_rows_kernel<C>, mw[0], mw[1], mx, a);
   (void)e;  // also kept for cudaGetLastError, which the check reads
   GPTQ_LAUNCH_CHECK();
   return GPTQ_OK;
 }
 
+// The row kernel's 8-bit output goes through rows of fp32 in the workspace.
+int64_t w4a8_scratch_pitch(int64_t d_row) { return (d_row + 127) / 128 * 128; }
+
 template <int NL, int NT>
-gptq_status w4a8_rows(const w4a8::Params& p, int num_sms, cudaStream_t s) {
+gptq_status w4a8_rows(w4a8::Params p, int num_sms, float* scratch, cudaStream_t s) {
+  if (p.out == GPTQ_I8) {
+    w4a8::Params q = p;
+    q.y = scratch;
+    q.ldy = w4a8_scratch_pitch(p.d_row);
+    q.out = GPTQ_F32;
+    gptq_status st = w4a8_rows<NL, NT>(q, num_sms, nullptr, s);
+    if (st != GPTQ_OK) return st;
+    cudaLaunchConfig_t lc{};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    const int n = static_cast<int>(p.n);
+    lc.gridDim = dim3(static_cast<unsigned>(((p.d_row + 127) / 128 * n + 3) / 4));
+    lc.blockDim = dim3(128);
+    lc.stream = s;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&lc, w4a8::quant8_rows_kernel, (const float*)q.y, q.ldy, n,
+                                       p.d_row, static_cast<int8_t*>(p.y), p.ldy, p.ys);
+    (void)e;  // also kept for cudaGetLastError, which the check reads
+    GPTQ_LAUNCH_CHECK();
+    return GPTQ_OK;
+  }
   // a region of 32 RJ columns has one scale: with one scale a row, always;
   // else it must lie inside a group
   if (p.n_groups == 1 || p.group % 128 == 0) return w4a8_rows_launch<w4a8::Cfg<NL, 4, NT>>(p, num_sms, s);
@@ -741,8 +740,8 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
 template <bool GATED>
 gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gptq_config* cfg,
                          const int8_t* codes, int64_t ldq, const float* x_scales, int x_group,
-                         int64_t n, void* y, int y_type, int64_t ldy, float* y_scales,
-                         void* stream) {
+                         int64_t n, void* y, int y_type, int64_t ldy, float* y_scales, void* ws,
+                         size_t ws_bytes, void* stream) {
   if (d_row < 1 || d_row > (int64_t(1) << 24) || d_col < 32 || d_col % 32 != 0 || d_col > 65536)
     return GPTQ_ERR_INVALID;
   if (!config_ok(cfg, d_col) || cfg->bits != 4) return GPTQ_ERR_INVALID;
@@ -759,6 +758,9 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
     return GPTQ_ERR_INVALID;
   if (!aligned(y, y_type == GPTQ_F32 ? 4 : y_type == GPTQ_BF16 ? 2 : 1)) return GPTQ_ERR_INVALID;
   if (y_type == GPTQ_I8 && (!y_scales || !aligned(y_scales, 4))) return GPTQ_ERR_INVALID;
+  const size_t need = gptq_w4a8_workspace_size(n, d_row, y_type);
+  if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return GPTQ_ERR_WORKSPACE;
+  float* scratch = static_cast<float*>(ws);
   p.x = codes;
   p.xs = x_scales;
   p.y = y;
@@ -779,8 +781,8 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
   if (st != GPTQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using Cf = W4a8Cfg<GATED>;
-  if (n <= 8) return w4a8_rows<Cf::NL, 1>(p, num_sms, s);
-  if (n <= 16) return w4a8_rows<Cf::NL, 2>(p, num_sms, s);
+  if (n <= 8) return w4a8_rows<Cf::NL, 1>(p, num_sms, scratch, s);
+  if (n <= 16) return w4a8_rows<Cf::NL, 2>(p, num_sms, scratch, s);
   if (n <= Cf::Small::TN) return w4a8_tiled<typename Cf::Small>(p, num_sms, s);
   const int64_t big = w4a8_tiles<typename Cf::Big>(p);
   if (n > Cf::Mid::TN && big >= num_sms) return w4a8_tiled<typename Cf::Big>(p, num_sms, s);
@@ -791,6 +793,11 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
 
 extern "C" {
 
+size_t gptq_w4a8_workspace_size(int64_t n, int64_t d_row, int h_type) {
+  if (h_type != GPTQ_I8 || n < 1 || n > 16 || d_row < 1 || d_row > (int64_t(1) << 24)) return 0;
+  return align_up(static_cast<size_t>(n) * w4a8_scratch_pitch(d_row) * 4);
+}
+
 gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const uint8_t* zeros,
                              int64_t d_row, int64_t d_col, const gptq_config* cfg,
                              const int8_t* codes, int64_t ldq, const float* x_scales, int x_group,
@@ -798,7 +805,7 @@ gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const
   w4a8::Params p{};
   p.layer[0] = w4a8::Layer{qweight, scales, zeros};
   return w4a8_product<false>(p, d_row, d_col, cfg, codes, ldq, x_scales, x_group, n, Y, y_type,
-                             ldy, nullptr, stream);
+                             ldy, nullptr, nullptr, 0, stream);
 }
 
 gptq_status gptq_w4a8_gated(const uint32_t* qweight_gate, const float* scales_gate,
@@ -806,12 +813,13 @@ gptq_status gptq_w4a8_gated(const uint32_t* qweight_gate, const float* scales_ga
                             const float* scales_up, const uint8_t* zeros_up, int64_t d_row,
                             int64_t d_col, const gptq_config* cfg, const int8_t* codes,
                             int64_t ldq, const float* x_scales, int x_group, int64_t n, void* H,
-                            int h_type, int64_t ldh, float* h_scales, void* stream) {
+                            int h_type, int64_t ldh, float* h_scales, void* ws, size_t ws_bytes,
+                            void* stream) {
   w4a8::Params p{};
   p.layer[0] = w4a8::Layer{qweight_gate, scales_gate, zeros_gate};
   p.layer[1] = w4a8::Layer{qweight_up, scales_up, zeros_up};
   return w4a8_product<true>(p, d_row, d_col, cfg, codes, ldq, x_scales, x_group, n, H, h_type,
-                            ldh, h_scales, stream);
+                            ldh, h_scales, ws, ws_bytes, stream);
 }
 
 gptq_status gptq_awq_channel_scale(const void* X, int64_t n, int64_t d, int64_t ldx, double* sx,

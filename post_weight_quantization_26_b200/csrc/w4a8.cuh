@@ -29,7 +29,6 @@
 // zero points are loaded one chunk ahead.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "act8.cuh"
@@ -37,8 +36,6 @@
 
 namespace gptq {
 namespace w4a8 {
-
-namespace cg = cooperative_groups;
 
 constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_I8 = 2;  // == GPTQ_F32, GPTQ_BF16, GPTQ_I8
 constexpr int WARPS = 8;     // computing warps
@@ -93,16 +90,13 @@ template <int NL_, int RJ_, int NT_>
 struct Cfg {
   static constexpr int NL = NL_, RJ = RJ_, NT = NT_;
   static constexpr int ROWS = NL == 2 ? 16 : 32;  // rows of each layer per CTA
-  static constexpr int CLUSTER = 128 / ROWS;      // CTAs that share 128 output columns
   static constexpr int W_BYTES = 32 * 128 * CPS / 2;  // both tiles' words of a stage
   static constexpr int X_BYTES = 8 * NT * 128;        // the tokens' codes of one chunk
   static constexpr int STAGE_BYTES = W_BYTES + CPS * X_BYTES;
   static constexpr int MINB = 2;
   static constexpr int RED_BYTES = WARPS * NT * 32 * 16;  // the warps' sums of one 16-row tile
-  static constexpr int TOP_BYTES = 2 * CLUSTER * 8 * NT * 4;
-  static constexpr int S = (227 * 1024 / MINB - RED_BYTES - TOP_BYTES - 3072) / STAGE_BYTES;
-  static constexpr int SMEM = S * STAGE_BYTES + RED_BYTES + TOP_BYTES + (2 * S + 2) * 8 + 16 +
-                              1024 /* alignment */;
+  static constexpr int S = (227 * 1024 / MINB - RED_BYTES - 3072) / STAGE_BYTES;
+  static constexpr int SMEM = S * STAGE_BYTES + RED_BYTES + 2 * S * 8 + 16 + 1024 /* alignment */;
   static_assert(S >= 2, "stages");
   static_assert((SMEM + 1024) * MINB <= 228 * 1024, "shared memory");
 };
@@ -113,25 +107,6 @@ struct Launch {
   int tiles;  // blocks of ROWS rows
   int whole;  // the tokens' map is 3-D: columns of a chunk, chunks, tokens
 };
-
-// Arrive on the barrier at this address of a CTA of the cluster, after the
-// caller's and (through a CTA barrier) its CTA's writes there.
-__device__ __forceinline__ void arrive_peer(uint32_t bar, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 r;\n\t"
-      "mapa.shared::cluster.u32 r, %0, %1;\n\t"
-      "fence.acq_rel.cluster;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar),
-      "r"(rank)
-      : "memory");
-}
-// Wait for the peers' arrivals and what they wrote before; bounded.
-__device__ __forceinline__ bool wait_peers(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                           uint64_t limit_ns) {
-  const bool ok = mbar_wait_bounded(bar, parity, abort_flag, limit_ns);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return ok;
-}
 
 template <class C>
 __global__ void __launch_bounds__(THREADS, C::MINB)
@@ -146,11 +121,9 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   const uint32_t ring = (raw + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (ring - raw);
   float* red = reinterpret_cast<float*>(base + S * C::STAGE_BYTES);  // [warp][NT][32][4]
-  // maxima of the cluster's CTAs, two sets in turn: [set][rank][token]
-  uint32_t* tops = reinterpret_cast<uint32_t*>(base + S * C::STAGE_BYTES + C::RED_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * S + 2);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, tops0 = empty0 + 8u * S;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + S * C::STAGE_BYTES + C::RED_BYTES);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * S);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -158,16 +131,15 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       mbar_init(full0 + 8u * s, 1);
       mbar_init(empty0 + 8u * s, WARPS);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(tops0 + 8u * s, C::CLUSTER);
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmap_w0);
     if (NL == 2) tma_prefetch_desc(&tmap_w1);
     tma_prefetch_desc(&tmap_x);
   }
-  const bool codes = NL == 2 && p.out == OUT_I8;  // then the launch has clusters
-  if (codes) cg::this_cluster().sync();  // the peers' barriers stand before any arrival
-  else __syncthreads();
+  // what follows on the stream may be launched, to wait for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
 
   const int nchunks = (p.d_col + 127) >> 7;
   const int stages = (nchunks + CPS - 1) / CPS;
@@ -181,7 +153,6 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     uint32_t issued = 0;
     for (int tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
       const int row0 = tile * ROWS;
-      if (row0 >= p.d_row) continue;  // fills up the cluster
       for (int s = 0; s < stages; ++s) {
         ok = mbar_wait_bounded(empty0 + 8u * st, ph ^ 1u, abort_flag, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -218,164 +189,160 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     float acc[2][NT][4];
     const float* sp[2][2];
     const uint8_t* zp[2][2];
-    uint32_t set = 0;
     for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    const int row0 = tile * ROWS;
-    // rows past the layer take its last row's scales and are never written
+      const int row0 = tile * ROWS;
+      // rows past the layer take its last row's scales and are never written
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = min(row0 + (NL == 2 ? 0 : 16 * i) + g + 8 * h, p.d_row - 1);
-        const Layer& L = p.layer[NL == 2 ? i : 0];
-        sp[i][h] = L.scales + static_cast<size_t>(row) * p.n_groups;
-        zp[i][h] = L.zeros + static_cast<size_t>(row) * p.n_groups;
-      }
-    struct Scales {
-      float sx[NT][2], s[2][2][NREG];
-      uint32_t z[2][2][NREG];
-    };
-    auto load = [&](int c, Scales& k) {
-      const int cx = p.xgroups == 1 ? 0 : min(c, nchunks - 1);
+        for (int h = 0; h < 2; ++h) {
+          const int row = min(row0 + (NL == 2 ? 0 : 16 * i) + g + 8 * h, p.d_row - 1);
+          const Layer& L = p.layer[NL == 2 ? i : 0];
+          sp[i][h] = L.scales + static_cast<size_t>(row) * p.n_groups;
+          zp[i][h] = L.zeros + static_cast<size_t>(row) * p.n_groups;
+        }
+      struct Scales {
+        float sx[NT][2], s[2][2][NREG];
+        uint32_t z[2][2][NREG];
+      };
+      auto load = [&](int c, Scales& k) {
+        const int cx = p.xgroups == 1 ? 0 : min(c, nchunks - 1);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          k.sx[n][e] = __ldg(p.xs + static_cast<int64_t>(min(8 * n + 2 * t + e, ntok - 1)) * p.xgroups + cx);
+          for (int e = 0; e < 2; ++e)
+            k.sx[n][e] = __ldg(p.xs + static_cast<int64_t>(min(8 * n + 2 * t + e, ntok - 1)) * p.xgroups + cx);
 #pragma unroll
-      for (int m = 0; m < NREG; ++m) {
-        const int gi =
-            min(static_cast<int>(__umulhi(128 * c + 32 * RJ * m, p.gmagic)), p.n_groups - 1);
+        for (int m = 0; m < NREG; ++m) {
+          const int gi =
+              min(static_cast<int>(__umulhi(128 * c + 32 * RJ * m, p.gmagic)), p.n_groups - 1);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            k.s[i][h][m] = __ldg(sp[i][h] + gi);
-            k.z[i][h][m] = __ldg(zp[i][h] + gi);
-          }
-      }
-    };
-    // One chunk; with whole chunks the scales of the warp's next one are on
-    // the way meanwhile, into registers of their own: a copy would wait.
-    auto chunk = [&](int c, int slot, Scales& k, Scales& knext) {
-      if (RJ == 4) load(c + WARPS, knext);
-      else load(c, k);
-      if (__all_sync(0xffffffffu, ok) && c < nchunks) {
-        // 128-byte swizzle: 16-byte piece q of row r lies at q ^ (r & 7)
-        const uint8_t* wt = base + st * C::STAGE_BYTES + (slot >> 1) * 4096 + g * 128;
-        const int q0 = 4 * (slot & 1);
-        const uint8_t* xt = base + st * C::STAGE_BYTES + C::W_BYTES +
-                            (a.whole ? g * (CPS * 128) + slot * 128 : slot * C::X_BYTES + g * 128);
-        const int xg = a.whole ? 8 * CPS * 128 : 1024, xr = a.whole ? slot & 7 : g;
-        uint32_t w[2][2][4];
+            for (int h = 0; h < 2; ++h) {
+              k.s[i][h][m] = __ldg(sp[i][h] + gi);
+              k.z[i][h][m] = __ldg(zp[i][h] + gi);
+            }
+        }
+      };
+      // One chunk; with whole chunks the scales of the warp's next one are on
+      // the way meanwhile, into registers of their own: a copy would wait.
+      auto chunk = [&](int c, int slot, Scales& k, Scales& knext) {
+        if (RJ == 4) load(c + WARPS, knext);
+        else load(c, k);
+        if (__all_sync(0xffffffffu, ok) && c < nchunks) {
+          // 128-byte swizzle: 16-byte piece q of row r lies at q ^ (r & 7)
+          const uint8_t* wt = base + st * C::STAGE_BYTES + (slot >> 1) * 4096 + g * 128;
+          const int q0 = 4 * (slot & 1);
+          const uint8_t* xt = base + st * C::STAGE_BYTES + C::W_BYTES +
+                              (a.whole ? g * (CPS * 128) + slot * 128 : slot * C::X_BYTES + g * 128);
+          const int xg = a.whole ? 8 * CPS * 128 : 1024, xr = a.whole ? slot & 7 : g;
+          uint32_t w[2][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t* from = wt + (16 * i + 8 * h) * 128;
-            if (RJ == 4) {  // words 4 t .. 4 t + 3: the k order inside a chunk is free
-              const uint4 v = *reinterpret_cast<const uint4*>(from + (((q0 + t) ^ g) << 4));
-              w[i][h][0] = v.x; w[i][h][1] = v.y; w[i][h][2] = v.z; w[i][h][3] = v.w;
-            } else {  // word 4 j + t
+            for (int h = 0; h < 2; ++h) {
+              const uint8_t* from = wt + (16 * i + 8 * h) * 128;
+              if (RJ == 4) {  // words 4 t .. 4 t + 3: the k order inside a chunk is free
+                const uint4 v = *reinterpret_cast<const uint4*>(from + (((q0 + t) ^ g) << 4));
+                w[i][h][0] = v.x; w[i][h][1] = v.y; w[i][h][2] = v.z; w[i][h][3] = v.w;
+              } else {  // word 4 j + t
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  w[i][h][j] = *reinterpret_cast<const uint32_t*>(from + (((q0 + j) ^ g) << 4) + 4 * t);
+              }
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            uint2 x[4];  // the activations of the lane's words
+            const uint8_t* from = xt + n * xg;
+            if (RJ == 4) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint4 v = *reinterpret_cast<const uint4*>(from + (((2 * t + j) ^ xr) << 4));
+                x[2 * j] = make_uint2(v.x, v.y);
+                x[2 * j + 1] = make_uint2(v.z, v.w);
+              }
+            } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                w[i][h][j] = *reinterpret_cast<const uint32_t*>(from + (((q0 + j) ^ g) << 4) + 4 * t);
+                x[j] = *reinterpret_cast<const uint2*>(from + (((2 * j + (t >> 1)) ^ xr) << 4) + 8 * (t & 1));
             }
-          }
+            uint32_t b0[4], b1[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          uint2 x[4];  // the activations of the lane's words
-          const uint8_t* from = xt + n * xg;
-          if (RJ == 4) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint4 v = *reinterpret_cast<const uint4*>(from + (((2 * t + j) ^ xr) << 4));
-              x[2 * j] = make_uint2(v.x, v.y);
-              x[2 * j + 1] = make_uint2(v.z, v.w);
+            for (int j = 0; j < 4; ++j) {
+              b0[j] = __byte_perm(x[j].x, x[j].y, 0x6420);
+              b1[j] = __byte_perm(x[j].x, x[j].y, 0x7531);
             }
-          } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              x[j] = *reinterpret_cast<const uint2*>(from + (((2 * j + (t >> 1)) ^ xr) << 4) + 8 * (t & 1));
-          }
-          uint32_t b0[4], b1[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            b0[j] = __byte_perm(x[j].x, x[j].y, 0x6420);
-            b1[j] = __byte_perm(x[j].x, x[j].y, 0x7531);
-          }
-#pragma unroll
-          for (int m = 0; m < NREG; ++m) {
-            int sums[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = RJ * m; j < RJ * m + RJ; ++j)
-              mma_u8s8(sums, 0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u, b0[j], b1[j]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              int prod[4] = {0, 0, 0, 0};
+            for (int m = 0; m < NREG; ++m) {
+              int sums[4] = {0, 0, 0, 0};
 #pragma unroll
               for (int j = RJ * m; j < RJ * m + RJ; ++j)
-                mma_u8s8(prod, even_codes(w[i][0][j]), even_codes(w[i][1][j]), odd_codes(w[i][0][j]),
-                         odd_codes(w[i][1][j]), b0[j], b1[j]);
+                mma_u8s8(sums, 0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u, b0[j], b1[j]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[i][n][e] = fmaf(k.s[i][e >> 1][m] * k.sx[n][e & 1],
-                                    static_cast<float>(prod[e] - static_cast<int>(k.z[i][e >> 1][m]) * sums[e]),
-                                    acc[i][n][e]);
+              for (int i = 0; i < 2; ++i) {
+                int prod[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = RJ * m; j < RJ * m + RJ; ++j)
+                  mma_u8s8(prod, even_codes(w[i][0][j]), even_codes(w[i][1][j]), odd_codes(w[i][0][j]),
+                           odd_codes(w[i][1][j]), b0[j], b1[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  acc[i][n][e] = fmaf(k.s[i][e >> 1][m] * k.sx[n][e & 1],
+                                      static_cast<float>(prod[e] - static_cast<int>(k.z[i][e >> 1][m]) * sums[e]),
+                                      acc[i][n][e]);
+              }
             }
           }
         }
-      }
-    };
-    auto stage = [&](int s, Scales& k, Scales& knext) {
-      if (s >= stages) return;
-      ok = ok && mbar_wait_bounded(full0 + 8u * st, ph, abort_flag, a.wait_ns);
-      chunk(s * CPS + warp, warp, k, knext);
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
-      if (++st == S) { st = 0; ph ^= 1u; }
-    };
-    if (row0 < p.d_row) {
+      };
+      auto stage = [&](int s, Scales& k, Scales& knext) {
+        if (s >= stages) return;
+        ok = ok && mbar_wait_bounded(full0 + 8u * st, ph, abort_flag, a.wait_ns);
+        chunk(s * CPS + warp, warp, k, knext);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(empty0 + 8u * st);
+        if (++st == S) { st = 0; ph ^= 1u; }
+      };
       Scales k0, k1;
       if (RJ == 4) load(warp, k0);
       for (int s = 0; s < stages; s += 2) {
         stage(s, k0, k1);
         stage(s + 1, k1, k0);
       }
-    }
 
-    // The sums over the warps, one 16-row tile at a time; a thread gets the
-    // outputs tid, tid + 256, ... of 16 rows x 8 NT tokens.  Element e of lane
-    // l of a fragment is row (l >> 2) + 8 (e >> 1) of its tile, token
-    // 2 (l & 3) + (e & 1) of its group of eight.
-    constexpr int OUTS = (16 * 8 * NT + 32 * WARPS - 1) / (32 * WARPS);
-    float v[2][OUTS];
+      // The sums over the warps, one 16-row tile at a time; a thread gets the
+      // outputs tid, tid + 256, ... of 16 rows x 8 NT tokens.  Element e of lane
+      // l of a fragment is row (l >> 2) + 8 (e >> 1) of its tile, token
+      // 2 (l & 3) + (e & 1) of its group of eight.
+      constexpr int OUTS = (16 * 8 * NT + 32 * WARPS - 1) / (32 * WARPS);
+      float v[2][OUTS];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      named_bar(1, 32 * WARPS);  // the last sums have been read
+      for (int i = 0; i < 2; ++i) {
+        named_bar(1, 32 * WARPS);  // the last sums have been read
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float4*>(red + ((warp * NT + n) * 32 + lane) * 4) =
-            make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
-      named_bar(1, 32 * WARPS);
+        for (int n = 0; n < NT; ++n)
+          *reinterpret_cast<float4*>(red + ((warp * NT + n) * 32 + lane) * 4) =
+              make_float4(acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]);
+        named_bar(1, 32 * WARPS);
 #pragma unroll
-      for (int j = 0; j < OUTS; ++j) {
-        const int o = threadIdx.x + j * 32 * WARPS, rl = o & 15, tk = o >> 4;
-        v[i][j] = 0.0f;
-        if (tk < ntok)
+        for (int j = 0; j < OUTS; ++j) {
+          const int o = threadIdx.x + j * 32 * WARPS, rl = o & 15, tk = o >> 4;
+          v[i][j] = 0.0f;
+          if (tk < ntok)
 #pragma unroll
-          for (int w = 0; w < WARPS; ++w)
-            v[i][j] += red[((w * NT + (tk >> 3)) * 32 + (rl & 7) * 4 + ((tk & 7) >> 1)) * 4 +
-                           2 * (rl >> 3) + (tk & 1)];
+            for (int w = 0; w < WARPS; ++w)
+              v[i][j] += red[((w * NT + (tk >> 3)) * 32 + (rl & 7) * 4 + ((tk & 7) >> 1)) * 4 +
+                             2 * (rl >> 3) + (tk & 1)];
+        }
       }
-    }
-    if (NL == 1 || !codes) {
 #pragma unroll
       for (int j = 0; j < OUTS; ++j) {
         const int o = threadIdx.x + j * 32 * WARPS, row = row0 + (o & 15), tk = o >> 4;
@@ -387,45 +354,35 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           if (row + 16 < p.d_row) store_out(p, tk * p.ldy + row + 16, v[1][j]);
         }
       }
-    } else {
-      // 8-bit output: half a warp has a token's 16 rows; each CTA of the
-      // cluster tells the others its maxima over the block of 128 columns.  A
-      // set is free again when it comes round: a peer that writes it for the
-      // next tile but one has seen this CTA's arrival for the next.
-      const uint32_t at = set & 1u;
-      float h[OUTS];
-      cg::cluster_group cl = cg::this_cluster();
-      const uint32_t rank = cl.block_rank();
-#pragma unroll
-      for (int j = 0; j < OUTS; ++j) {
-        const int o = threadIdx.x + j * 32 * WARPS, tk = o >> 4;
-        const bool live = tk < ntok && row0 + (o & 15) < p.d_row;
-        h[j] = live ? silu_times(v[0][j], v[1][j]) : 0.0f;
-        const uint32_t top =
-            __reduce_max_sync(lane & 16 ? 0xffff0000u : 0x0000ffffu, act8::abs_bits(h[j]));
-        if (tk < ntok && (lane & 15) < C::CLUSTER)  // a lane a peer
-          *cl.map_shared_rank(&tops[(at * C::CLUSTER + rank) * 8 * NT + tk], lane & 15) = top;
-      }
-      named_bar(1, 32 * WARPS);
-      if (threadIdx.x < C::CLUSTER) arrive_peer(tops0 + 8u * at, threadIdx.x);
-      ok = ok && wait_peers(tops0 + 8u * at, (set >> 1) & 1u, abort_flag, a.wait_ns);
-      ++set;
-#pragma unroll
-      for (int j = 0; j < OUTS; ++j) {
-        const int o = threadIdx.x + j * 32 * WARPS, tk = o >> 4, row = row0 + (o & 15);
-        if (tk >= ntok || row >= p.d_row) continue;
-        uint32_t top = 0;
-#pragma unroll
-        for (int r = 0; r < C::CLUSTER; ++r) top = max(top, tops[(at * C::CLUSTER + r) * 8 * NT + tk]);
-        const act8::Quant q = act8::quant_of(top);
-        static_cast<int8_t*>(p.y)[tk * p.ldy + row] = static_cast<int8_t>(act8::code_or_zero(h[j], q));
-        if (row % 128 == 0) p.ys[tk * static_cast<int64_t>((p.d_row + 127) / 128) + row / 128] = q.scale;
-      }
-    }
     }
   }
-  __syncthreads();
-  if (codes) cg::this_cluster().sync();  // no CTA leaves while another may still write its maxima
+}
+
+// The 8-bit form of fp32 rows, a warp a token and block of 128 columns.  It
+// stands behind the row kernel on the stream, whose CTAs hold 16 rows of a
+// block each: clusters that exchange their maxima would have to lie within a
+// GPC, which leaves 33 of 37 room and a fifth of the SMs idle (61 us for one
+// token through a gated pair of 22016 x 8192 that takes 44 without).
+__global__ void __launch_bounds__(128) quant8_rows_kernel(const float* __restrict__ h, int64_t ldh,
+                                                          int n, int d, int8_t* codes, int64_t ldq,
+                                                          float* scales) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int blocks = (d + 127) / 128;
+  const int lane = threadIdx.x & 31;
+  const int at = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (at >= blocks * n) return;
+  const int tk = at / blocks, col = (at % blocks) * 128 + 4 * lane;
+  const float4 f = *reinterpret_cast<const float4*>(h + tk * ldh + col);  // rows are whole blocks
+  const float v[4] = {f.x, f.y, f.z, f.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < d) top = max(top, act8::abs_bits(v[i]));
+  const act8::Quant q = act8::quant_of(__reduce_max_sync(0xffffffffu, top));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (col + i < d) codes[tk * ldq + col + i] = static_cast<int8_t>(act8::code_or_zero(v[i], q));
+  if (lane == 0) scales[at] = q.scale;
 }
 
 }  // namespace w4a8

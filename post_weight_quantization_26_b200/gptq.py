@@ -28,7 +28,7 @@ EXPORTED = ("gptq_workspace_size", "gptq_hessian_accumulate",
             "gptq_device_status", "gptq_status_string", "gptq_launch_count",
             "gptq_dequant_check_noalloc", "gptq_w4a16_matmul", "gptq_awq_channel_scale",
             "gptq_awq_workspace_size", "gptq_awq_search",
-            "gptq_rmsnorm_quant8", "gptq_w4a8_matmul", "gptq_w4a8_gated")
+            "gptq_rmsnorm_quant8", "gptq_w4a8_matmul", "gptq_w4a8_workspace_size", "gptq_w4a8_gated")
 NOALLOC_MAX_TILES = 65536  # GPTQ_NOALLOC_MAX_TILES in include/gptq.h
 ACT_GROUP = 128  # columns that share an activation scale, where a token has several
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.int8: 2}  # gptq_dtype in include/gptq.h
@@ -99,8 +99,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gptq_rmsnorm_quant8.restype = I
     lib.gptq_w4a8_matmul.argtypes = [P, P, P, I64, I64, cfgp, P, I64, P, I, I64, P, I, I64, P]
     lib.gptq_w4a8_matmul.restype = I
+    lib.gptq_w4a8_workspace_size.argtypes = [I64, I64, I]
+    lib.gptq_w4a8_workspace_size.restype = SZ
     lib.gptq_w4a8_gated.argtypes = [P, P, P, P, P, P, I64, I64, cfgp, P, I64, P, I, I64, P, I,
-                                    I64, P, P]
+                                    I64, P, P, SZ, P]
     lib.gptq_w4a8_gated.restype = I
     lib.gptq_awq_channel_scale.argtypes = [P, I64, I64, I64, P, P]
     lib.gptq_awq_channel_scale.restype = I
@@ -295,46 +297,47 @@ def _elsewhere(t, stream):
     """None where a call on tensor t runs on the current stream of t's device
     and that device is current; else the context to make the call in.  Outputs
     that the call allocates then belong to the stream that it runs on."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
         return torch.cuda.stream(stream)
-    return None if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+    return None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
 
 
-def _one_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
+def _rows(name, t, dtypes, n, d, dev):
+    """The row stride of an n x d matrix on device `dev` whose rows are dense.
+    (These checks run on every call of a generation's token, where they cost as
+    much as the kernel, so they are kept short.)"""
+    if t.dtype not in dtypes or t.shape != (n, d) or t.get_device() != dev:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected one of "
+                         f"{dtypes} {(n, d)} on cuda:{dev}")
+    s0, s1 = t.stride()
+    if (s1 != 1 and d > 1) or (s0 < d and n > 1):
+        raise ValueError(f"{name}: rows must be dense, strides {(s0, s1)}")
+    return s0 if n > 1 else max(d, s0)
 
 
-def _rows(name, t, dtypes, shape):
-    """The row stride of a matrix of a given shape whose rows are dense."""
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtypes} {tuple(shape)}")
-    n, d = shape
-    if (d > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < d):
-        raise ValueError(f"{name}: rows must be dense, strides {t.stride()}")
-    return t.stride(0) if n > 1 else max(d, t.stride(0))
-
-
-def _dense(name, t, dtypes, shape):
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous {dtypes} "
-                         f"{tuple(shape)}")
+def _dense(name, t, dtypes, shape, dev):
+    if (t.dtype not in dtypes or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous, "
+                         f"one of {dtypes} {tuple(shape)} on cuda:{dev}")
 
 
 def alloc_codes(n: int, d: int, group: int = ACT_GROUP, device="cuda"):
     """8-bit activations n x d: int8 codes (row stride a multiple of 16, as
     the products need it) and fp32 scales."""
-    codes = torch.empty((n, (d + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :d]
-    return codes, torch.empty((n, -(-d // group) if group else 1), dtype=torch.float32,
-                              device=device)
+    pitch = (d + 15) // 16 * 16
+    codes = torch.empty((n, pitch), dtype=torch.int8, device=device)
+    return (codes if pitch == d else codes[:, :d],
+            torch.empty((n, -(-d // group) if group else 1), dtype=torch.float32, device=device))
 
 
-_FLOATS = (torch.float32, torch.bfloat16)
+_FLOATS, _F32 = (torch.float32, torch.bfloat16), (torch.float32,)
+_I8, _U8, _WORDS = (torch.int8,), (torch.uint8,), (torch.int32, torch.uint32)
 
 
 def gptq_rmsnorm_quant8(X, weight, eps: float = 1e-6, residual=None, group: int = ACT_GROUP,
@@ -353,50 +356,53 @@ def gptq_rmsnorm_quant8(X, weight, eps: float = 1e-6, residual=None, group: int 
     if X.dim() != 2:
         raise ValueError("X must be n x d")
     n, d = X.shape
+    dev = X.get_device()
     codes, scales = alloc_codes(n, d, group, X.device) if out is None else out
-    _one_device(X, weight, residual, residual_out, codes, scales)
-    ldx = _rows("X", X, _FLOATS, (n, d))
-    ldq = _rows("codes", codes, (torch.int8,), (n, d))
-    _dense("scales", scales, (torch.float32,), (n, -(-d // ACT_GROUP) if group else 1))
-    if weight is not None:
-        _dense("weight", weight, (torch.float32,), (d,))
+    ldx = _rows("X", X, _FLOATS, n, d, dev)
+    ldq = _rows("codes", codes, _I8, n, d, dev)
+    _dense("scales", scales, _F32, (n, -(-d // ACT_GROUP) if group else 1), dev)
+    wp = rp = op = None
     r_type = ldr = ldo = 0
+    if weight is not None:
+        _dense("weight", weight, _F32, (d,), dev)
+        wp = weight.data_ptr()
     if residual is not None:
         if residual_out is None:
             residual_out = torch.empty((n, d), dtype=residual.dtype, device=X.device)
-        ldr = _rows("residual", residual, _FLOATS, (n, d))
-        ldo = _rows("residual_out", residual_out, (residual.dtype,), (n, d))
-        r_type = DTYPES[residual.dtype]
+        ldr = _rows("residual", residual, _FLOATS, n, d, dev)
+        ldo = _rows("residual_out", residual_out, (residual.dtype,), n, d, dev)
+        r_type, rp, op = DTYPES[residual.dtype], residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    st = load_library().gptq_rmsnorm_quant8(
-        X.data_ptr(), DTYPES[X.dtype], ldx, None if residual is None else residual.data_ptr(),
-        r_type, ldr, None if weight is None else weight.data_ptr(), eps, n, d, group,
-        None if residual is None else residual_out.data_ptr(), ldo, codes.data_ptr(), ldq,
-        scales.data_ptr(), _stream(None))
-    _check(st, "gptq_rmsnorm_quant8")
+    st = (_lib or load_library()).gptq_rmsnorm_quant8(
+        X.data_ptr(), DTYPES[X.dtype], ldx, rp, r_type, ldr, wp, eps, n, d, group, op, ldo,
+        codes.data_ptr(), ldq, scales.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise GptqError(st, "gptq_rmsnorm_quant8")
     return (codes, scales) if residual is None else (codes, scales, residual_out)
 
 
-def _w4a8_args(layers, cfg, codes, x_scales):
-    """Checks what both products share; returns (n, d_row, d_col, ldq, x_group)."""
-    if codes.dim() != 2:
-        raise ValueError("codes must be n x d_col")
+def _layer_args(layer, cfg, d_row, d_col, dev):
+    """Checks a packed layer; returns its three pointers."""
+    qweight, scales, zeros = layer
+    groups = (d_row, n_groups(d_col, cfg.group_size))
+    _dense("qweight", qweight, _WORDS, (d_row, d_col // 8), dev)
+    _dense("scales", scales, _F32, groups, dev)
+    _dense("zeros", zeros, _U8, groups, dev)
+    return qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr()
+
+
+def _codes_args(codes, x_scales, dev):
+    """Checks 8-bit activations; returns (n, d_col, ldq, x_group)."""
+    if codes.dim() != 2 or x_scales.dim() != 2:
+        raise ValueError("codes must be n x d_col, x_scales n x blocks")
     n, d_col = codes.shape
-    ldq = _rows("codes", codes, (torch.int8,), (n, d_col))
+    ldq = _rows("codes", codes, _I8, n, d_col, dev)
     if n <= 1:
         ldq = (ldq + 15) // 16 * 16  # the stride of one row is not used
-    blocks = -(-d_col // ACT_GROUP)
-    x_group = 0 if x_scales.dim() == 2 and x_scales.shape[1] == 1 else ACT_GROUP
-    _dense("x_scales", x_scales, (torch.float32,), (n, blocks if x_group else 1))
-    d_row = layers[0][1].shape[0]
-    _one_device(codes, x_scales, *(t for layer in layers for t in layer))
-    ng = n_groups(d_col, cfg.group_size)
-    for qweight, scales, zeros in layers:
-        _dense("qweight", qweight, (torch.int32, torch.uint32), (d_row, d_col // 8))
-        _dense("scales", scales, (torch.float32,), (d_row, ng))
-        _dense("zeros", zeros, (torch.uint8,), (d_row, ng))
-    return n, d_row, d_col, ldq, x_group
+    x_group = 0 if x_scales.shape[1] == 1 else ACT_GROUP
+    _dense("x_scales", x_scales, _F32, (n, -(-d_col // ACT_GROUP) if x_group else 1), dev)
+    return n, d_col, ldq, x_group
 
 
 def gptq_w4a8_matmul(qweight, scales, zeros, cfg: GptqConfig, codes, x_scales, Y=None,
@@ -409,44 +415,65 @@ def gptq_w4a8_matmul(qweight, scales, zeros, cfg: GptqConfig, codes, x_scales, Y
     if place is not None:
         with place:
             return gptq_w4a8_matmul(qweight, scales, zeros, cfg, codes, x_scales, Y, dtype)
-    n, d_row, d_col, ldq, x_group = _w4a8_args([(qweight, scales, zeros)], cfg, codes, x_scales)
+    dev = codes.get_device()
+    n, d_col, ldq, x_group = _codes_args(codes, x_scales, dev)
+    d_row = scales.shape[0]
+    qw, sc, ze = _layer_args((qweight, scales, zeros), cfg, d_row, d_col, dev)
     if Y is None:
         Y = torch.empty((n, d_row), dtype=dtype, device=codes.device)
-    _one_device(codes, Y)
-    ldy = _rows("Y", Y, _FLOATS, (n, d_row))
-    st = load_library().gptq_w4a8_matmul(
-        qweight.data_ptr(), scales.data_ptr(), zeros.data_ptr(), d_row, d_col, ctypes.byref(cfg),
-        codes.data_ptr(), ldq, x_scales.data_ptr(), x_group, n, Y.data_ptr(), DTYPES[Y.dtype], ldy,
-        _stream(None))
-    _check(st, "gptq_w4a8_matmul")
+    ldy = _rows("Y", Y, _FLOATS, n, d_row, dev)
+    st = (_lib or load_library()).gptq_w4a8_matmul(
+        qw, sc, ze, d_row, d_col, cfg, codes.data_ptr(), ldq, x_scales.data_ptr(), x_group, n,
+        Y.data_ptr(), DTYPES[Y.dtype], ldy, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise GptqError(st, "gptq_w4a8_matmul")
     return Y
 
 
+def gptq_w4a8_workspace_size(n: int, d_row: int, dtype) -> int:
+    """Bytes of workspace of gptq_w4a8_gated for n tokens and an output type."""
+    return int(load_library().gptq_w4a8_workspace_size(n, d_row, DTYPES[dtype]))
+
+
 def gptq_w4a8_gated(gate, up, cfg: GptqConfig, codes, x_scales, out=None, dtype=torch.bfloat16,
-                    stream=None):
+                    ws=None, stream=None):
     """H = silu(X Wg^T) * (X Wu^T) for 8-bit activations and two packed 4-bit
     layers, each (qweight, scales, zeros).  dtype float32 or bfloat16: returns
     H (n x d_row), which `out` may give; int8: returns H as (codes, scales)
-    with a scale per token and 128 columns, which `out` may give as a pair."""
+    with a scale per token and 128 columns, which `out` may give as a pair.
+    `ws` (uint8, gptq_w4a8_workspace_size bytes) is allocated when not given."""
     place = _elsewhere(codes, stream)
     if place is not None:
         with place:
-            return gptq_w4a8_gated(gate, up, cfg, codes, x_scales, out, dtype)
-    n, d_row, d_col, ldq, x_group = _w4a8_args([gate, up], cfg, codes, x_scales)
+            return gptq_w4a8_gated(gate, up, cfg, codes, x_scales, out, dtype, ws)
+    dev = codes.get_device()
+    n, d_col, ldq, x_group = _codes_args(codes, x_scales, dev)
+    d_row = gate[1].shape[0]
+    layers = (*_layer_args(gate, cfg, d_row, d_col, dev), *_layer_args(up, cfg, d_row, d_col, dev))
     if out is None:
         out = (alloc_codes(n, d_row, ACT_GROUP, codes.device) if dtype == torch.int8 else
                torch.empty((n, d_row), dtype=dtype, device=codes.device))
     H, h_scales = out if isinstance(out, (tuple, list)) else (out, None)
-    _one_device(codes, H, h_scales)
-    ldh = _rows("H", H, _FLOATS if h_scales is None else (torch.int8,), (n, d_row))
+    ldh = _rows("H", H, _FLOATS if h_scales is None else _I8, n, d_row, dev)
+    hs = None
     if h_scales is not None:
-        _dense("h_scales", h_scales, (torch.float32,), (n, -(-d_row // ACT_GROUP)))
-    st = load_library().gptq_w4a8_gated(
-        gate[0].data_ptr(), gate[1].data_ptr(), gate[2].data_ptr(), up[0].data_ptr(),
-        up[1].data_ptr(), up[2].data_ptr(), d_row, d_col, ctypes.byref(cfg), codes.data_ptr(), ldq,
-        x_scales.data_ptr(), x_group, n, H.data_ptr(), DTYPES[H.dtype], ldh,
-        None if h_scales is None else h_scales.data_ptr(), _stream(None))
-    _check(st, "gptq_w4a8_gated")
+        _dense("h_scales", h_scales, _F32, (n, -(-d_row // ACT_GROUP)), dev)
+        hs = h_scales.data_ptr()
+    h_type = DTYPES[H.dtype]
+    lib = _lib or load_library()
+    need = lib.gptq_w4a8_workspace_size(n, d_row, h_type)
+    wp, ws_bytes = None, 0
+    if need:
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=codes.device)
+        elif ws.dtype != torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous uint8 on the tensors' device")
+        wp, ws_bytes = ws.data_ptr(), ws.numel()
+    st = lib.gptq_w4a8_gated(
+        *layers, d_row, d_col, cfg, codes.data_ptr(), ldq, x_scales.data_ptr(), x_group, n,
+        H.data_ptr(), h_type, ldh, hs, wp, ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise GptqError(st, "gptq_w4a8_gated")
     return out
 
 

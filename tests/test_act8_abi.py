@@ -52,8 +52,8 @@ def _matmul(G, cfg=None, **bad):
 
 def _gated(G, cfg=None, **bad):
     a = dict(qg=FAKE, sg=FAKE, zg=FAKE, qw=FAKE, s=FAKE, z=FAKE, d_row=64, d_col=256, cfg=cfg,
-             codes=FAKE, ldq=256, xs=FAKE, xg=128, n=4, Y=FAKE, y_type=0, ldy=64, hs=FAKE,
-             stream=None)
+             codes=FAKE, ldq=256, xs=FAKE, xg=128, n=4, Y=FAKE, y_type=0, ldy=64, hs=FAKE, ws=FAKE,
+             ws_bytes=1 << 20, stream=None)
     a.update(bad)
     return G.load_library().gptq_w4a8_gated(*a.values())
 
@@ -87,6 +87,19 @@ def test_products_refuse_configurations(G):
     assert _matmul(G, None) == 1 and _gated(G, None) == 1
 
 
+def test_gated_workspace(G):
+    """Only an 8-bit output of up to 16 tokens needs one: fp32 rows of whole
+    blocks of 128."""
+    size = G.load_library().gptq_w4a8_workspace_size
+    assert size(1, 64, 2) == 512 and size(16, 129, 2) == 16 * 256 * 4
+    for none in ((17, 64, 2), (16, 64, 1), (16, 64, 0), (0, 64, 2), (-1, 64, 2), (4, 0, 2),
+                 (4, (1 << 24) + 1, 2)):
+        assert size(*none) == 0
+    cfg = ctypes.byref(G.make_config(bits=4, group_size=128))
+    for bad in (dict(ws=None), dict(ws=off(128)), dict(ws_bytes=2047)):
+        assert _gated(G, cfg, y_type=2, **bad) == 4
+
+
 def test_products_of_no_tokens(G):
     cfg = ctypes.byref(G.make_config(bits=4))
     assert _matmul(G, cfg, n=0, codes=None, xs=None, Y=None) == 0
@@ -114,11 +127,14 @@ def test_alloc_codes_pitch(G):
 def test_binding_shape_checks(G):
     """The checks that stand behind the device check."""
     t = torch.zeros(4, 64)
-    assert G._rows("t", t, (torch.float32,), (4, 64)) == 64
-    assert G._rows("t", t[:, :32], (torch.float32,), (4, 32)) == 64
-    assert G._rows("t", t[:1, :32], (torch.float32,), (1, 32)) == 64
+    f32 = (torch.float32,)
+    assert G._rows("t", t, f32, 4, 64, -1) == 64
+    assert G._rows("t", t[:, :32], f32, 4, 32, -1) == 64
+    assert G._rows("t", t[:1, :32], f32, 1, 32, -1) == 64
     for bad in (t.T, t.bfloat16(), t[:, ::2], t[:1].expand(4, 64), t[:2]):
         with pytest.raises(ValueError):
-            G._rows("t", bad, (torch.float32,), (4, 64))
+            G._rows("t", bad, f32, 4, 64, -1)
     with pytest.raises(ValueError):
-        G._dense("t", t[:, :32], (torch.float32,), (4, 32))
+        G._rows("t", t, f32, 4, 64, 0)  # another device
+    with pytest.raises(ValueError):
+        G._dense("t", t[:, :32], f32, (4, 32), -1)
