@@ -66,7 +66,7 @@ struct Cfg {
   static constexpr int SW_BYTES = NS * 4 * NL * BM * 4;  // of row scales, four a row
   static constexpr int Z_BYTES = NS * NL * BM * 4;       // of zero points, four in a word
   static constexpr int TOP_BYTES = BIG && NL == 2 ? 4 * TN * 4 : 0;
-  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 2 * NS + 1;
+  static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 2 * NS + 2;
   static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + Z_BYTES + TOP_BYTES +
                               BARS * 8 + 16 + 1024 /* alignment */;
   static_assert(NU >= NL && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
@@ -294,12 +294,17 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                  tempty0 = tfull0 + 8u * NU, sfull0 = tempty0 + 8u * NU, sempty0 = sfull0 + 8u * C::NS,
                  drain = sempty0 + 8u * C::NS;
 
+  // Each chunk's last run closes its TMEM buffer, or runs span chunks.  Where
+  // they close, two MMA warps take the operand slots in turn, provided that
+  // they use different buffers (their waits tell phases by parity alone).
+  const bool every = p.xgroups != 1 || a.runs != 1 || p.group == CH;
+  const bool turns = every && NU % (2 * a.runs) == 0;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool leader = elect_one();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, 1);
-      mbar_init(empty0 + 8u * s, 8 * NL + 1);  // unpacked, and multiplied
+      mbar_init(empty0 + 8u * s, 8 * NL + (turns ? 2 : 1));  // unpacked, and multiplied
     }
     for (int s = 0; s < AS; ++s) {
       mbar_init(afull0 + 8u * s, 4);
@@ -310,10 +315,11 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       mbar_init(tempty0 + 8u * u, EW);
     }
     for (int u = 0; u < C::NS; ++u) {
-      mbar_init(sfull0 + 8u * u, 64);  // the scale warps' lanes
+      mbar_init(sfull0 + 8u * u, 64);  // the scale warp's lanes and their copies
       mbar_init(sempty0 + 8u * u, UW + EW);
     }
     mbar_init(drain, 1);
+    mbar_init(drain + 8u, 1);
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tmap_w0);
@@ -340,7 +346,6 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   const int64_t tile0 = C::BIG ? blockIdx.x : blockIdx.x / a.ksplit;
   const int64_t tile_step = C::BIG ? gridDim.x : tiles;
   // a chunk's last run closes its TMEM buffer unless neither scale changes
-  const bool every = p.xgroups != 1 || a.runs != 1 || p.group == CH;
   auto group_of = [&](int col) {
     return min(static_cast<int>(__umulhi(static_cast<uint32_t>(col), p.gmagic)), p.n_groups - 1);
   };
@@ -387,24 +392,25 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           mbar_wait_bounded(full0 + 8u * (i % S), (i / S) & 1u, &own, a.wait_ns);
         }
       }
-    } else if (warp == UW + EW + 1) {
-      // ------------------------------------------------------------ MMA warp
+    } else if (warp <= UW + EW + 2) {
+      // ----------------------------------------------------------- MMA warps
+      const uint32_t mw = warp - (UW + EW + 1);
       const uint64_t DESC = smem_desc_sw128(0, 16, 1024);  // addresses are added
-      uint32_t st = 0, slot = 0, sph = 0, unit = 0;
-      bool open = false;  // the current buffers hold a started run
+      uint32_t st = 0, k = 0, unit = 0;  // stage, slots and TMEM buffers so far
+      bool open = false;                 // the current buffers hold a started run
       for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
         for (int c = c0; c < c1 && ok; ++c) {
           const bool close = closes(c);
           // The tokens' codes came with the words that the unpack warps waited
-          // for, so their arrival stands for both: a wait costs this warp 170
-          // clocks even where there is nothing to wait for, a third of what a
-          // chunk may take.
+          // for, so their arrival stands for both.
           const uint64_t xd = DESC + ((ring + st * C::STAGE_BYTES + NL * PACKED_BYTES +
                                        (c & 1) * C::X_BYTES) >> 4);
 #pragma unroll
-          for (int l = 0; l < NL; ++l) {
+          for (int l = 0; l < NL; ++l, ++k) {
+            if (turns ? (k & 1u) != mw : mw != 0) continue;
+            const uint32_t slot = k % AS;
             const uint64_t ad = DESC + ((slots + slot * SLOT_BYTES) >> 4);
-            W4T_WAIT(afull0 + 8u * slot, sph);
+            W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
             // 32 columns are 32 bytes: 2 units of a descriptor's address
             if (a.runs == 1) {
               const uint32_t u = unit + l, buf = u % NU, d = tmem_base + buf * TN;
@@ -412,8 +418,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
               tc_fence_after();
               if (ok && leader) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_i8_ss(d, ad + 2 * k, xd + 2 * k, IDESC, k != 0 || open);
+                for (int i = 0; i < 4; ++i) mma_i8_ss(d, ad + 2 * i, xd + 2 * i, IDESC, i != 0 || open);
                 if (close) mma_commit(tfull0 + 8u * buf);
               }
             } else {
@@ -432,32 +437,31 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                 }
               }
             }
-            if (ok && leader) mma_commit(aempty0 + 8u * slot);
-            if (++slot == AS) { slot = 0; sph ^= 1u; }
+            if (ok && leader) {
+              mma_commit(aempty0 + 8u * slot);
+              // after the warp's last slot of the stage
+              if (turns ? NL == 1 || (c & 1) : (c & 1) && l == NL - 1) mma_commit(empty0 + 8u * st);
+            }
+            __syncwarp();
           }
-          if (c & 1) {
-            if (ok && leader) mma_commit(empty0 + 8u * st);
-            if (++st == S) st = 0;
-          }
-          __syncwarp();
+          if ((c & 1) && ++st == S) st = 0;
           open = !close;
           if (close) unit += NL * a.runs;
         }
       }
       if (!ok && leader) {  // given up: the tensor cores are done before TMEM is freed
         int own = 0;
-        mma_commit(drain);
-        mbar_wait_bounded(drain, 0, &own, a.wait_ns);
+        mma_commit(drain + 8u * mw);
+        mbar_wait_bounded(drain + 8u * mw, 0, &own, a.wait_ns);
       }
     } else {
-      // --------------------------------------------------------- scale warps
+      // ---------------------------------------------------------- scale warp
       // The scales and zero points of the next runs, in sets of four runs (4,
       // 2 or 1 chunks), and those chunks' token scales: a lane copies a row's
       // or token's four at once where they lie in 16 aligned bytes, straight
       // to shared memory and NS sets ahead, as row scales come from HBM.  (One
       // value at a time and line took more of the load unit than all else, 640
       // clocks a chunk of 128 x 256 outputs.)
-      const int i = threadIdx.x - (UW + EW + 2) * 32;  // 0..63
       const int per_set = 4 / a.runs, step = CH / a.runs;
       uint32_t set = 0;
       for (int64_t t = tile0; t < tiles; t += tile_step) {
@@ -470,44 +474,50 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           const bool xvec = a.xvec && (cs & 3) == 0 && cs + 4 <= p.xgroups;
           const bool wvec = a.wvec && (g[0] & 3) == 0 && g[3] == g[0] + 3;
           W4T_WAIT(sempty0 + 8u * at, ((set / NS) & 1u) ^ 1u);
-          if (ok) {
-            for (int r = i; r < TN; r += 64) {
-              const float* from = p.xs + min(tok0 + r, p.n - 1) * p.xgroups;
-              float* to = sx + (at * TN + r) * 4;
-              if (xvec) {
-                copy_async<16>(to, from + cs);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  copy_async<4>(to + j, from + (p.xgroups == 1 ? 0 : min(cs + j, nchunks - 1)));
-              }
-            }
-#pragma unroll
-            for (int l = 0; l < NL; ++l)
-              for (int r = i; r < BM; r += 64) {
-                const size_t first = static_cast<size_t>(min(row0 + r, p.d_row - 1)) * p.n_groups;
-                const float* sf = p.layer[l].scales + first;
-                const uint8_t* zf = p.layer[l].zeros + first;
-                float* to = swb + ((at * NL + l) * BM + r) * 4;
-                uint32_t* zt = zb + (at * NL + l) * BM + r;
-                if (wvec) {
-                  copy_async<16>(to, sf + g[0]);
-                  copy_async<4>(zt, zf + g[0]);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) copy_async<4>(to + j, sf + g[j]);
-                  *zt = __ldg(zf + g[0]) | (__ldg(zf + g[1]) << 8) | (__ldg(zf + g[2]) << 16) |
-                        (static_cast<uint32_t>(__ldg(zf + g[3])) << 24);
-                }
-              }
-            if (wvec) {  // the copies' own arrival, when they are done
-              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8u * at)
-                           : "memory");
+          if (!ok) continue;
+#pragma unroll 1
+          for (int r = lane; r < TN; r += 32) {
+            const float* from = p.xs + min(tok0 + r, p.n - 1) * p.xgroups;
+            float* to = sx + (at * TN + r) * 4;
+            if (xvec) {
+              copy_async<16>(to, from + cs);
             } else {
-              asm volatile("cp.async.wait_all;" ::: "memory");
-              mbar_arrive(sfull0 + 8u * at);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                copy_async<4>(to + j, from + (p.xgroups == 1 ? 0 : min(cs + j, nchunks - 1)));
             }
           }
+#pragma unroll
+          for (int l = 0; l < NL; ++l) {
+            uint32_t z[BM / 32][4];
+#pragma unroll
+            for (int i = 0; i < BM / 32; ++i) {
+              const int r = lane + 32 * i;
+              const size_t first = static_cast<size_t>(min(row0 + r, p.d_row - 1)) * p.n_groups;
+              const float* sf = p.layer[l].scales + first;
+              const uint8_t* zf = p.layer[l].zeros + first;
+              float* to = swb + ((at * NL + l) * BM + r) * 4;
+              if (wvec) {
+                copy_async<16>(to, sf + g[0]);
+                copy_async<4>(zb + (at * NL + l) * BM + r, zf + g[0]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  copy_async<4>(to + j, sf + g[j]);
+                  z[i][j] = __ldg(zf + g[j]);
+                }
+              }
+            }
+            if (!wvec)
+#pragma unroll
+              for (int i = 0; i < BM / 32; ++i)
+                zb[(at * NL + l) * BM + lane + 32 * i] =
+                    z[i][0] | (z[i][1] << 8) | (z[i][2] << 16) | (z[i][3] << 24);
+          }
+          // the copies arrive when they are done, the lane for its own stores
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8u * at)
+                       : "memory");
+          mbar_arrive(sfull0 + 8u * at);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
