@@ -84,7 +84,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sum (or maximum of bits) over the block; every thread gets it.  `buf` has
-// one word per warp and is free again after the next block-wide barrier.
+// one word per warp and is free again after the next block-wide barrier (a loop
+// takes two in turn).
 __device__ __forceinline__ float block_sum(float v, float* buf) {
   v = warp_sum(v);
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -105,15 +106,6 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
 }
 // Round v to the type, store it, and leave the rounded values in v.
 __device__ __forceinline__ void store8(float* p, float (&v)[8]) {
@@ -142,85 +134,111 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[8], const Quant& q) {
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
-// Aligned rows of whole vectors of eight: one block a token, NV vectors a
-// thread in registers, so the pass reads and writes each byte once and is
-// bound by HBM (16384 x 8192 bf16 with residual: 939 MB).  Sixteen lanes hold
-// a group of 128 columns.
-template <typename TX, typename TR, int NV>
-__global__ void __launch_bounds__(NV == 8 ? 512 : 1024 / NV) rmsnorm_quant8_kernel(const Params p) {
-  __shared__ float sums[32];
-  __shared__ uint32_t tops[32];
-  const int64_t t = blockIdx.x;
-  const int nvec = p.d >> 3;
-  const TX* x = static_cast<const TX*>(p.x) + t * p.ldx;
-  float v[NV][8], r[8];
-  float sum = 0.0f;
+// Eight elements as they are in memory.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = threadIdx.x + i * blockDim.x;
-    if (k < nvec) load8(x + 8 * k, v[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-  if (p.res) {
-    const TR* res = static_cast<const TR*>(p.res) + t * p.ldr;
-    TR* out = static_cast<TR*>(p.res_out) + t * p.ldo;
+  __device__ __forceinline__ float at(int j) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+    if (sizeof(T) == 4) return __uint_as_float(w[j]);
+    return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  }
+};
+
+// Aligned rows of whole vectors of eight: a block a token, NV vectors a thread
+// in registers, so the pass reads and writes each byte once and is bound by
+// HBM: 16384 x 8192 bf16 with residual, 939 MB, in 176 us, 5.3 TB/s.  A block
+// takes rows blockIdx.x, + gridDim.x, ... and has the next row's loads on the way
+// while it reduces and writes the current one (AHEAD; 205 us with a block a row).
+// Rows of more than 8192 columns take more threads, and then the registers do not
+// hold a second row.  Sixteen lanes
+// hold a group of 128 columns.  res_out may be the memory of x or of the
+// residual: a row is loaded whole before it is stored, and no row's loads reach
+// into another's.
+template <typename TX, typename TR, int NV, bool AHEAD>
+__global__ void __launch_bounds__(AHEAD ? 1024 / NV : 1024) rmsnorm_quant8_kernel(const Params p) {
+  __shared__ float sums[2][32];
+  __shared__ uint32_t tops[2][32];
+  const int nvec = p.d >> 3;
+  Raw8<TX> rx[AHEAD ? NV : 1];
+  Raw8<TR> rr[AHEAD ? NV : 1];
+  auto fetch = [&](int64_t t, int i, Raw8<TX>& x, Raw8<TR>& r) {
+    const int k = threadIdx.x + i * blockDim.x;
+    if (k >= nvec) return;
+    x.load(static_cast<const TX*>(p.x) + t * p.ldx + 8 * k);
+    if (p.res) r.load(static_cast<const TR*>(p.res) + t * p.ldr + 8 * k);
+  };
+  int64_t t = blockIdx.x;
+  if (AHEAD)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) fetch(t, i, rx[i], rr[i]);
+  for (int turn = 0; t < p.n; turn ^= 1) {
+    float v[NV][8], r[8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = threadIdx.x + i * blockDim.x, b = AHEAD ? i : 0;
+      if (!AHEAD) fetch(t, i, rx[0], rr[0]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = k < nvec ? rx[b].at(j) : 0.0f;
+      if (p.res && k < nvec) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += rr[b].at(j);
+        store8(static_cast<TR*>(p.res_out) + t * p.ldo + 8 * k, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += v[i][j] * v[i][j];
+    }
+    const int64_t now = t;
+    t += gridDim.x;
+    if (AHEAD && t < p.n)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) fetch(t, i, rx[i], rr[i]);
+    sum = block_sum(sum, sums[turn]);
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
+    uint32_t top[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int k = threadIdx.x + i * blockDim.x;
-      if (k < nvec) {
-        load8(res + 8 * k, r);
+      if (p.weight && k < nvec) {
+        load8(p.weight + 8 * k, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-        store8(out + 8 * k, v[i]);
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * r[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
       }
+      top[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top[i] = max(top[i], abs_bits(v[i][j]));
+      if (k >= nvec) top[i] = 0;  // 0 * infinity
     }
-  }
+    int8_t* codes = p.codes + now * p.ldq;
+    if (p.n_groups == 1) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int i = 1; i < NV; ++i) top[0] = max(top[0], top[i]);
+      const Quant q = quant_of(block_max(top[0], tops[turn]));
+      if (threadIdx.x == 0) p.scales[now] = q.scale;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum += v[i][j] * v[i][j];
-  sum = block_sum(sum, sums);
-  const float rstd = 1.0f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
-  uint32_t top[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int k = threadIdx.x + i * blockDim.x;
-    if (p.weight && k < nvec) {
-      load8(p.weight + 8 * k, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * r[j];
+      for (int i = 0; i < NV; ++i) {
+        const int k = threadIdx.x + i * blockDim.x;
+        if (k < nvec) *reinterpret_cast<uint2*>(codes + 8 * k) = codes8(v[i], q);
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
-    }
-    top[i] = 0;
+      for (int i = 0; i < NV; ++i) {
+        const int k = threadIdx.x + i * blockDim.x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[i] = max(top[i], abs_bits(v[i][j]));
-    if (k >= nvec) top[i] = 0;  // 0 * infinity
-  }
-  int8_t* codes = p.codes + t * p.ldq;
-  if (p.n_groups == 1) {
-#pragma unroll
-    for (int i = 1; i < NV; ++i) top[0] = max(top[0], top[i]);
-    const Quant q = quant_of(block_max(top[0], tops));
-    if (threadIdx.x == 0) p.scales[t] = q.scale;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = threadIdx.x + i * blockDim.x;
-      if (k < nvec) *reinterpret_cast<uint2*>(codes + 8 * k) = codes8(v[i], q);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = threadIdx.x + i * blockDim.x;
-#pragma unroll
-      for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-      const Quant q = quant_of(top[i]);
-      if (k < nvec) {
-        *reinterpret_cast<uint2*>(codes + 8 * k) = codes8(v[i], q);
-        if ((k & 15) == 0) p.scales[t * p.n_groups + (k >> 4)] = q.scale;
+        for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        const Quant q = quant_of(top[i]);
+        if (k < nvec) {
+          *reinterpret_cast<uint2*>(codes + 8 * k) = codes8(v[i], q);
+          if ((k & 15) == 0) p.scales[now * p.n_groups + (k >> 4)] = q.scale;
+        }
       }
     }
   }
