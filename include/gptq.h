@@ -279,7 +279,8 @@ gptq_status gptq_w4a16_matmul(const uint32_t* qweight, const float* scales,
                               const gptq_config* cfg, const void* X, int64_t batch,
                               float* Y, void* stream);
 
-/* Element types of the calls below. */
+/* Element types of the calls below.  As with the other calls, the first one on
+ * a device sets the library up there; make it before any stream capture. */
 typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_I8 = 2 } gptq_dtype;
 
 /* 8-bit activations, as the three calls below write and read them (the
@@ -307,7 +308,7 @@ typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_I8 = 2 } gptq_dtype;
  *                or NULL: r = X and residual_out is not written.
  *  weight        fp32[d], or NULL for ones.  The per-channel scale of
  *                gptq_awq_search is applied by dividing weight by s*.
- *  eps           >= 0 and finite.
+ *  eps           >= 0 and finite (with 0, a token of zeros gives NaN scales).
  *  group         0 or 128, the x_group above.
  *  residual_out  n x d, row stride ldo, type r_type; it may be X or residual
  *                itself (same pointer, stride and type), else the arrays do

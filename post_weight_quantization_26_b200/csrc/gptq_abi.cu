@@ -502,14 +502,14 @@ namespace {
 
 // NV vectors of eight a thread: one for few tokens, where only latency counts
 // and a row wants many threads; up to four for many, with more bytes in flight a
-// thread.  With many rounds of blocks, as many as are on the GPU at once take
-// the rows in turn and load ahead; with few, a block has a row (777 x 4096:
-// 4.6 us, with loads ahead 5.4; 16384 x 8192: 205 us, with loads ahead 172).
-template <typename TX, typename TR, int NV, bool AHEAD>
-gptq_status norm_rows(const act8::Params& p, int num_sms, cudaStream_t s) {
+// thread.  With many rounds of blocks (`turns`), as many as are on the GPU at
+// once take the rows in turn and load ahead; with few, a block has a row (777 x
+// 4096: 5.4 us against 5.8; 16384 x 8192: 205 us against 172).
+template <typename TX, typename TR, int NV, bool AHEAD = true>
+gptq_status norm_rows(const act8::Params& p, bool turns, int num_sms, cudaStream_t s) {
   const int nvec = p.d / 8, threads = ((nvec + NV - 1) / NV + 31) / 32 * 32;
   int64_t grid = p.n;
-  if (AHEAD) {
+  if (turns) {
     int per_sm = 0;
     GPTQ_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(
         &per_sm, act8::rmsnorm_quant8_kernel<TX, TR, NV, AHEAD>, threads, 0));
@@ -523,18 +523,17 @@ gptq_status norm_rows(const act8::Params& p, int num_sms, cudaStream_t s) {
 template <typename TX, typename TR>
 gptq_status norm_launch(const act8::Params& p, bool fast, int num_sms, cudaStream_t s) {
   const int nvec = p.d / 8;
-  const bool many = p.n > 16 * num_sms;
+  const bool turns = p.n > 16 * num_sms;
   if (!fast) {
     act8::rmsnorm_quant8_any_kernel<TX, TR><<<static_cast<unsigned>(p.n), 256, 0, s>>>(p);
     GPTQ_LAUNCH_CHECK();
     return GPTQ_OK;
   }
-  if (nvec <= 1024 && (p.n <= num_sms || nvec <= 128))
-    return many ? norm_rows<TX, TR, 1, true>(p, num_sms, s) : norm_rows<TX, TR, 1, false>(p, num_sms, s);
-  if (nvec <= 512)
-    return many ? norm_rows<TX, TR, 2, true>(p, num_sms, s) : norm_rows<TX, TR, 2, false>(p, num_sms, s);
-  if (nvec <= 1024 && many) return norm_rows<TX, TR, 4, true>(p, num_sms, s);
-  return norm_rows<TX, TR, 4, false>(p, num_sms, s);
+  if (nvec <= 1024 && (p.n <= num_sms || nvec <= 128)) return norm_rows<TX, TR, 1>(p, turns, num_sms, s);
+  if (nvec <= 512) return norm_rows<TX, TR, 2>(p, turns, num_sms, s);
+  if (nvec <= 1024) return norm_rows<TX, TR, 4>(p, turns, num_sms, s);
+  // more than 256 threads do not have the registers for a second row
+  return norm_rows<TX, TR, 4, false>(p, false, num_sms, s);
 }
 
 }  // namespace
@@ -574,8 +573,8 @@ gptq_status gptq_rmsnorm_quant8(const void* X, int x_type, int64_t ldx, const vo
   p.n_groups = group ? (p.d + act8::GROUP - 1) / act8::GROUP : 1;
   p.eps = eps_f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Whole, aligned vectors of eight elements keep a row in registers; up to
-  // 32768 columns fit.
+  // Whole, aligned vectors of eight elements keep a row in registers, up to
+  // 32768 columns.
   auto vectors = [](const void* q, int64_t ld, size_t bytes, size_t unit) {
     return aligned(q, unit) && (ld * static_cast<int64_t>(bytes)) % static_cast<int64_t>(unit) == 0;
   };
@@ -800,6 +799,11 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
   if (st != GPTQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using Cf = W4a8Cfg<GATED>;
+  // Up to 16 tokens the row kernel reads the weights fastest (16 tokens, 8192 x
+  // 22016: 34 us; 17 in tiles: 51).  A tile of 64 or 128 tokens costs nearly the
+  // same whatever it holds.  The persistent shape halves the unpacking a token
+  // and wants a tile for every SM (1024 tokens, 8192 x 22016: 363 us against 495
+  // in tiles of 128).
   if (n <= 8) return w4a8_rows<Cf::NL, 1>(p, num_sms, scratch, s);
   if (n <= 16) return w4a8_rows<Cf::NL, 2>(p, num_sms, scratch, s);
   if (n <= Cf::Small::TN) return w4a8_tiled<typename Cf::Small>(p, num_sms, s);

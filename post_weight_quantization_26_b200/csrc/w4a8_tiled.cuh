@@ -5,27 +5,38 @@
 // (kind::i8, int32 accumulators, exact).
 //
 // A tile is 128 rows of the layer (of both layers, for the gated pair) by TN
-// tokens.  The layer's rows are the M side, so the weight scale of a run is one
-// value a thread in the epilogue, and the tokens' scales are broadcast reads.
-// Work goes in chunks of 128 columns:
+// tokens, the layer's rows on the M side.  Work goes in chunks of 128 columns,
+// two to a stage:
 //
-//   TMA warp      packed rows (64 B a row and chunk, 64-byte swizzle) and the
-//                 tokens' codes (128 B, 128-byte swizzle) into a ring
+//   TMA warp      the rows' words (128 B a row and stage) and the tokens' codes
+//                 (two times 128 B), 128-byte swizzle, into a ring
 //   unpack warps  a thread has a row: words of eight codes -> q - z as signed
 //                 bytes in column order, into 128-byte-swizzled operand slots.
 //                 Bytes 0x80 + q - z never borrow from their neighbour, so four
-//                 codes cost an AND-OR, a subtraction, half of two PRMT, an XOR
-//   MMA warp      one thread issues tcgen05.mma, 32 columns each; a run (32, 64
+//                 codes cost an AND-OR, a subtraction, half of two PRMT, an XOR.
+//                 Groups of four warps take the slots in turn
+//   MMA warps     one thread issues tcgen05.mma, 32 columns each; a run (32, 64
 //                 or 128 columns, or more where no scale changes) starts from
 //                 zero in its own TMEM buffer
-//   epilogue      int32 -> fp32, times weight scale and token scale, added to
-//                 fp32 registers while the next runs are in the tensor cores
+//   scale warp    row scales, zero points and token scales of the next four
+//                 runs, copied to shared memory some sets ahead
+//   epilogue      int32 -> fp32, times row scale and token scale, added to fp32
+//                 registers while the next runs are in the tensor cores
 //
 // Every mbarrier wait is bounded, as in the Hessian kernel.
 //
-// Three shapes (Cfg): SMALL and MID have one tile a cluster of up to 8 CTAs
+// Three shapes (Cfg).  SMALL and MID have one tile a cluster of up to 8 CTAs
 // that split the chunks; their sums meet in shared memory of the cluster, in
 // rank order, so the result does not vary.  BIG is persistent, without a split.
+//
+// What bounds it (measured): 4096 tokens through 8192 x 22016 (groups of 128)
+// take 1.40 ms, 1.06 PFLOP/s, 0.64 of the bf16 rate that cuBLAS reaches.  The
+// MMAs would take 512 clocks a chunk of 128 x 256 outputs; with nothing but
+// copies, unpacking and MMAs a chunk takes 860, with the epilogue 1900: scaling
+// each run's sums costs a conversion, a product and a fused add an output, 512
+// clocks of each pipe, in chains that sixteen warps do not fully overlap.  More
+// epilogue warps in groups of their own, spreading the token scales by an MMA
+// with ones, and 128-token tiles were built and were slower.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -47,8 +58,8 @@ constexpr int SUM_PITCH = BM + 4;  // rows of a token's sums: spreads a warp's 8
 
 // NL: layers; TN: tokens per tile; UW, EW: unpack and epilogue warps; S: ring
 // stages; AS: operand slots of one layer and chunk; NS: sets of scales on the
-// way or in use; MORE: registers of an epilogue thread.  Four
-// more warps are the TMA warp, the MMA warp and two that fetch scales.
+// way or in use; MORE: registers of an epilogue thread.  Four more warps are the
+// TMA warp, two MMA warps and the scale warp.
 template <int NL_, int TN_, int UW_, int EW_, int S_, int AS_, int NS_, int MORE_, bool BIG_>
 struct Cfg {
   static constexpr int NL = NL_, TN = TN_, UW = UW_, EW = EW_, S = S_, AS = AS_, NS = NS_;
