@@ -110,14 +110,21 @@ template <class C>
 cudaError_t w4a8_allow_smem() {
   return allow_smem(w4a8t::w4a8_tiled_kernel<C>, C::SMEM);
 }
+template <class C>
+cudaError_t w4a8_allow_rows_shape() {
+  return allow_smem(w4a8::w4a8_rows_kernel<C>, C::SMEM);
+}
+template <int NL, int NT, bool STAGED>
+cudaError_t w4a8_allow_rows_runs() {
+  cudaError_t e = w4a8_allow_rows_shape<w4a8::Cfg<NL, 4, NT, STAGED>>();
+  if (e == cudaSuccess) e = w4a8_allow_rows_shape<w4a8::Cfg<NL, 2, NT, STAGED>>();
+  if (e == cudaSuccess) e = w4a8_allow_rows_shape<w4a8::Cfg<NL, 1, NT, STAGED>>();
+  return e;
+}
 template <int NL, int NT>
 cudaError_t w4a8_allow_rows() {
-  cudaError_t e = allow_smem(w4a8::w4a8_rows_kernel<w4a8::Cfg<NL, 4, NT>>, w4a8::Cfg<NL, 4, NT>::SMEM);
-  if (e == cudaSuccess)
-    e = allow_smem(w4a8::w4a8_rows_kernel<w4a8::Cfg<NL, 2, NT>>, w4a8::Cfg<NL, 2, NT>::SMEM);
-  if (e == cudaSuccess)
-    e = allow_smem(w4a8::w4a8_rows_kernel<w4a8::Cfg<NL, 1, NT>>, w4a8::Cfg<NL, 1, NT>::SMEM);
-  return e;
+  const cudaError_t e = w4a8_allow_rows_runs<NL, NT, true>();
+  return e != cudaSuccess ? e : w4a8_allow_rows_runs<NL, NT, false>();
 }
 
 std::mutex g_mu;
@@ -689,9 +696,18 @@ gptq_status w4a8_rows(w4a8::Params p, int num_sms, float* scratch, cudaStream_t 
   }
   // a region of 32 RJ columns has one scale: with one scale a row, always;
   // else it must lie inside a group
-  if (p.n_groups == 1 || p.group % 128 == 0) return w4a8_rows_launch<w4a8::Cfg<NL, 4, NT>>(p, num_sms, s);
-  if (p.group % 64 == 0) return w4a8_rows_launch<w4a8::Cfg<NL, 2, NT>>(p, num_sms, s);
-  return w4a8_rows_launch<w4a8::Cfg<NL, 1, NT>>(p, num_sms, s);
+  // and may come with the stages where it is a group by itself
+  bool in_fours = p.n_groups % 4 == 0 && aligned(p.xs, 16) && (p.xgroups == 1 || p.xgroups % 4 == 0);
+  for (int l = 0; l < NL; ++l)
+    in_fours = in_fours && aligned(p.layer[l].scales, 16) && aligned(p.layer[l].zeros, 4);
+  if (p.n_groups == 1 || p.group % 128 == 0)
+    return in_fours && p.group == 128 ? w4a8_rows_launch<w4a8::Cfg<NL, 4, NT, true>>(p, num_sms, s)
+                                      : w4a8_rows_launch<w4a8::Cfg<NL, 4, NT, false>>(p, num_sms, s);
+  if (p.group % 64 == 0)
+    return in_fours && p.group == 64 ? w4a8_rows_launch<w4a8::Cfg<NL, 2, NT, true>>(p, num_sms, s)
+                                     : w4a8_rows_launch<w4a8::Cfg<NL, 2, NT, false>>(p, num_sms, s);
+  return in_fours && p.group == 32 ? w4a8_rows_launch<w4a8::Cfg<NL, 1, NT, true>>(p, num_sms, s)
+                                   : w4a8_rows_launch<w4a8::Cfg<NL, 1, NT, false>>(p, num_sms, s);
 }
 
 template <class C>

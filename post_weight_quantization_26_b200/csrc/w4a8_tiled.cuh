@@ -48,6 +48,7 @@
 namespace gptq {
 namespace w4a8t {
 
+using w4a8::copy_async;
 using w4a8::Params;
 
 constexpr int BM = 128;  // layer rows per tile
@@ -116,15 +117,6 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
-}
-
-// 4 or 16 bytes into shared memory without passing through a register.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
 // Four signed bytes q - z of one word's even or odd codes, still biased by 128.
