@@ -311,8 +311,9 @@ typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_I8 = 2 } gptq_dtype;
  *  eps           >= 0 and finite (with 0, a token of zeros gives NaN scales).
  *  group         0 or 128, the x_group above.
  *  residual_out  n x d, row stride ldo, type r_type; it may be X or residual
- *                itself (same pointer, stride and type), else the arrays do
- *                not overlap.  Ignored without a residual.
+ *                itself (same pointer, stride and type; the same pointer with
+ *                another stride or type is refused), else the arrays do not
+ *                overlap.  Ignored without a residual.
  *  codes, ldq, scales   outputs as above; columns d .. ldq - 1 of a row are
  *                left as they were.
  * 0 <= n < 2^31 (n = 0 is a no-op), 1 <= d <= 65536; strides >= d; pointers

@@ -138,3 +138,13 @@ def test_binding_shape_checks(G):
         G._rows("t", t, f32, 4, 64, 0)  # another device
     with pytest.raises(ValueError):
         G._dense("t", t[:, :32], f32, (4, 32), -1)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(X=off(256), out=off(256), x_type=0), dict(X=off(256), out=off(256), ldx=72),
+    dict(X=off(256), out=off(256), r_type=0), dict(res=off(256), out=off(256), ldo=72),
+], ids=str)
+def test_norm_refuses_half_in_place(G, bad):
+    """residual_out in X's or the residual's memory needs its stride and type."""
+    good = dict(X=FAKE, res=off(1 << 20), out=off(1 << 21))
+    assert G.load_library().gptq_rmsnorm_quant8(*{**NORM, **good, **bad}.values()) == 1

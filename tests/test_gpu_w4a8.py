@@ -289,3 +289,32 @@ def test_refusals(G):
             G.gptq_w4a8_matmul(*L, cfg, view, scales[:view.shape[0]].contiguous())
     with pytest.raises(G.GptqError):
         G.gptq_w4a8_matmul(L[0], L[1], L[2], G.make_config(bits=3, group_size=64), codes, scales)
+
+
+def shifted(t):
+    """The same values at an address one element further."""
+    room = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    room[1:] = t.flatten()
+    return room[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("shape", [(77, 1536, 128), (161, 1024, 64), (45, 1920, 32), (130, 640, 128)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("n", [1, 8, 9, 16, 17, 64, 65, 130])
+@pytest.mark.parametrize("xg", [0, 128])
+def test_alignment_of_scales(G, shape, n, xg):
+    """Scales and zero points at any element's address: another way into the
+    kernels, the same order of sums, the same bits."""
+    rows, cols, group = shape
+    gate, up = small(layer(rows, cols, group, n)), small(layer(rows, cols, group, n + 1))
+    codes, scales = acts(n, cols, xg)
+    y = check_matmul(G, gate, group, codes, scales, F32)
+    h, hs = check_gated(G, gate, up, group, codes, scales, I8)
+    cfg = G.make_config(group_size=group)
+    moved = [(L[0], shifted(L[1]), shifted(L[2])) for L in (gate, up)]
+    for layers, s in ((moved, scales), ((gate, up), shifted(scales)), (moved, shifted(scales)),
+                      ((gate, moved[1]), scales)):
+        assert torch.equal(G.gptq_w4a8_matmul(*layers[0], cfg, codes, s), y)
+        h2, hs2 = G.gptq_w4a8_gated(*layers, cfg, codes, s, dtype=I8)
+        assert torch.equal(h2, h) and torch.equal(hs2, hs)
+    assert G.gptq_device_status() == 0
