@@ -822,7 +822,7 @@ gptq_status w4a8_product(w4a8::Params p, int64_t d_row, int64_t d_col, const gpt
   // Up to 16 tokens the row kernel reads the weights fastest (16 tokens, 8192 x
   // 22016: 30 us; 17 in tiles: 51).  A tile of 64 or 128 tokens costs nearly the
   // same whatever it holds.  The persistent shape halves the unpacking a token
-  // and wants a tile for every SM (1024 tokens, 8192 x 22016: 363 us against 495
+  // and wants a tile for every SM (1024 tokens, 8192 x 22016: 354 us against 495
   // in tiles of 128).
   if (n <= 8) return w4a8_rows<Cf::NL, 1>(p, num_sms, scratch, s);
   if (n <= 16) return w4a8_rows<Cf::NL, 2>(p, num_sms, scratch, s);

@@ -30,9 +30,9 @@
 // rank order, so the result does not vary.  BIG is persistent, without a split.
 //
 // What bounds it (measured): 4096 tokens through 8192 x 22016 (groups of 128)
-// take 1.40 ms, 1.06 PFLOP/s, 0.64 of the bf16 rate that cuBLAS reaches.  The
+// take 1.29 ms, 1.15 PFLOP/s, 0.70 of the bf16 rate that cuBLAS reaches.  The
 // MMAs would take 512 clocks a chunk of 128 x 256 outputs; with nothing but
-// copies, unpacking and MMAs a chunk takes 860, with the epilogue 1900: scaling
+// copies, unpacking and MMAs a chunk takes 860, with the epilogue 1750: scaling
 // each run's sums costs a conversion, a product and a fused add an output, 512
 // clocks of each pipe, in chains that sixteen warps do not fully overlap.  More
 // epilogue warps in groups of their own, spreading the token scales by an MMA
@@ -67,7 +67,9 @@ struct Cfg {
   static constexpr bool BIG = BIG_;
   static constexpr int WARPS = UW + EW + 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int NU = 512 / TN < 4 ? 512 / TN : 4;  // TMEM buffers
+  // TMEM buffers: with 8 two MMA warps take turns at four runs a chunk, too (61
+  // tokens, 4096 x 8192 in groups of 32: 29 us against 31 with 4)
+  static constexpr int NU = 512 / TN < 8 ? 512 / TN : 8;
   static constexpr int TMEM_COLS = NU * TN < 32 ? 32 : NU * TN;
   static constexpr int COLS = TN / (EW / 4);         // columns (tokens) per epilogue warp
   static constexpr int X_BYTES = TN * CH;
@@ -85,6 +87,8 @@ struct Cfg {
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
   static_assert(EW % 4 == 0 && UW % 4 == 0 && (COLS == 32 || COLS == 64), "warps");
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  // one CTA an SM, so no CTA of a cluster waits for TMEM that another holds
+  static_assert(2 * SMEM > 228 * 1024, "one CTA");
   // the launch's registers, THREADS x LAUNCH, move between warpgroups
   static constexpr int LAUNCH = 65536 / THREADS / 8 * 8, MORE = MORE_,
                        FEWER = (THREADS * LAUNCH - EW * 32 * MORE) / ((UW + 4) * 32) / 8 * 8;
@@ -221,51 +225,58 @@ __device__ __forceinline__ void store_rows8(const Params& p, int64_t at, const f
   }
 }
 
-// One run's sums, scaled and added; t0: the warp's lanes and first column in
-// TMEM, sw: its four rows' scales, sx: the first token's scale.  The reads of
-// TMEM are issued 32 columns and 16 lanes at a time, or all before the first is
-// used where the registers are there (ALL).  The conversion to fp32 is an
-// instruction of half the adders' rate; the add of 1.5 * 2^23 and its
-// subtraction would cost as much and more issue slots.
-template <int COLS>
-__device__ __forceinline__ void fold_32(Share<COLS>& acc, const uint32_t (&v)[16], int p, int h,
-                                        const float (&sw)[4], const uint64_t (&s)[4]) {
-#pragma unroll
-  for (int b = 0; b < 4; ++b)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint64_t f = pack2(__int2float_rn(static_cast<int>(v[4 * b + 2 * i])),
-                               __int2float_rn(static_cast<int>(v[4 * b + 2 * i + 1])));
-      uint64_t& a = acc.v[(h * (COLS / 8) + 4 * p + b) * 2 + i];
-      a = fma2(f, mul2(pack2(sw[2 * h + i], sw[2 * h + i]), s[b]), a);
-    }
+// 16 lanes x 16 columns: the same with two groups of eight columns.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
 }
-template <int COLS, bool ALL>
+
+// One run's sums, scaled and added; t0: the warp's lanes and first column in
+// TMEM, sw: its four rows' scales, sx: the first token's scale; `read` is called
+// when the last sums are in registers and the buffer may be written again (4096
+// tokens, 8192 x 22016: 1340 us, against 1420 with the buffer kept to the end).
+// TMEM is read in pieces of 16 lanes.  A warp of 64 tokens reads 16 columns at a
+// time with the next piece on the way while it folds one (1295 us); one of 32
+// tokens has two layers' sums or few pieces, and is faster with 32 columns at a
+// time (gated, 2048 tokens, 22016 x 8192: 1625 us against 1685).  The conversion
+// to fp32 is an instruction of half the adders' rate; the add of 1.5 * 2^23 and
+// its subtraction would cost as much and more issue slots.
+template <int COLS, class Read>
 __device__ __forceinline__ void fold_run(Share<COLS>& acc, uint32_t t0, const float (&sw)[4],
-                                         const float* sx) {
+                                         const float* sx, Read read) {
   const float* sxt = sx + 8 * (threadIdx.x & 3);  // four a token
-  constexpr int P = COLS / 32;
-  uint32_t v[ALL ? P : 1][ALL ? 2 : 1][16];
-  if (ALL) {
+  constexpr bool AHEAD = COLS == 64;
+  constexpr int W = AHEAD ? 16 : 32, N = 2 * COLS / W;  // piece k: columns W (k / 2), lanes 16 (k % 2)
+  uint32_t v[AHEAD ? 2 : 1][W / 2];
+  uint64_t s[W / 8];
+  auto load = [&](int k) {
+    tmem_ld_16x256b(t0 + (static_cast<uint32_t>(16 * (k & 1)) << 16) + W * (k >> 1), v[AHEAD ? k & 1 : 0]);
+  };
+  if (AHEAD) load(0);
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+  for (int k = 0; k < N; ++k) {
+    const int h = k & 1, c = W * (k >> 1);
+    if (!AHEAD) load(k);
+    if (h == 0)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        tmem_ld_16x256b(t0 + (static_cast<uint32_t>(16 * h) << 16) + 32 * p, v[p][h]);
-  }
+      for (int b = 0; b < W / 8; ++b) s[b] = pack2(sxt[4 * (c + 8 * b)], sxt[4 * (c + 8 * b) + 4]);
+    tmem_ld_wait();
+    if (k == N - 1) read();
+    else if (AHEAD) load(k + 1);
+    const uint32_t(&w)[W / 2] = v[AHEAD ? k & 1 : 0];
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    uint64_t s[4];
+    for (int b = 0; b < W / 8; ++b)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (!ALL) tmem_ld_16x256b(t0 + (static_cast<uint32_t>(16 * h) << 16) + 32 * p, v[0][0]);
-      if (h == 0)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          s[b] = pack2(sxt[4 * (32 * p + 8 * b)], sxt[4 * (32 * p + 8 * b) + 4]);
-      if (!ALL || (p == 0 && h == 0)) tmem_ld_wait();
-      fold_32<COLS>(acc, v[ALL ? p : 0][ALL ? h : 0], p, h, sw, s);
-    }
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t f = pack2(__int2float_rn(static_cast<int>(w[4 * b + 2 * i])),
+                                 __int2float_rn(static_cast<int>(w[4 * b + 2 * i + 1])));
+        uint64_t& o = acc.v[(h * (COLS / 8) + c / 8 + b) * 2 + i];
+        o = fma2(f, mul2(pack2(sw[2 * h + i], sw[2 * h + i]), s[b]), o);
+      }
   }
 }
 
@@ -622,10 +633,12 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
               W4T_WAIT(tfull0 + 8u * buf, (u / NU) & 1u);
               __syncwarp();  // the loads are the whole warp's, also after a wait that gave up
               tc_fence_after();
-              fold_run<COLS, (C::MORE >= 128)>(acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs);
-              tc_fence_before();
-              __syncwarp();
-              if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
+              fold_run<COLS>(
+                  acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs, [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
+                  });
             }
           }
           unit += NL * a.runs;
