@@ -27,7 +27,8 @@
 //
 // Three shapes (Cfg).  SMALL and MID have one tile a cluster of up to 8 CTAs
 // that split the chunks; their sums meet in shared memory of the cluster, in
-// rank order, so the result does not vary.  BIG is persistent, without a split.
+// rank order, so the result does not vary.  BIG is persistent, without a split;
+// for the gated pair half of its epilogue warps has gate, half has up.
 //
 // What bounds it (measured): 4096 tokens through 8192 x 22016 (groups of 128)
 // take 1.29 ms, 1.15 PFLOP/s, 0.70 of the bf16 rate that cuBLAS reaches.  The
@@ -71,7 +72,14 @@ struct Cfg {
   // tokens, 4096 x 8192 in groups of 32: 29 us against 31 with 4)
   static constexpr int NU = 512 / TN < 8 ? 512 / TN : 8;
   static constexpr int TMEM_COLS = NU * TN < 32 ? 32 : NU * TN;
+  static constexpr int NB = NU / NL;                 // of a layer
   static constexpr int COLS = TN / (EW / 4);         // columns (tokens) per epilogue warp
+  // While it folds, half of the warps has gate, half has up, twice the columns
+  // each, so that two chains of waits run beside each other and the reads of TMEM
+  // run ahead; they trade halves at the end of a tile (333 tokens, 11008 x 4096 in
+  // groups of 32: 245 us against 336; 2048 tokens, 22016 x 8192: 1589 against 1620).
+  static constexpr bool HALVES = BIG && NL == 2;
+  static constexpr int FCOLS = HALVES ? 2 * COLS : COLS;
   static constexpr int X_BYTES = TN * CH;
   static constexpr int STAGE_BYTES = NL * PACKED_BYTES + 2 * X_BYTES;
   static constexpr int RING_BYTES = S * STAGE_BYTES;
@@ -80,10 +88,11 @@ struct Cfg {
   static constexpr int SW_BYTES = NS * 4 * NL * BM * 4;  // of row scales, four a row
   static constexpr int Z_BYTES = NS * NL * BM * 4;       // of zero points, four in a word
   static constexpr int TOP_BYTES = BIG && NL == 2 ? 4 * TN * 4 : 0;
+  static constexpr int TRADE_BYTES = HALVES ? EW * 1024 : 0;
   static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 2 * NS + 2;
-  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + Z_BYTES + TOP_BYTES +
+  static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + Z_BYTES + TOP_BYTES + TRADE_BYTES +
                               BARS * 8 + 16 + 1024 /* alignment */;
-  static_assert(NU >= NL && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
+  static_assert(NB >= 1 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
   static_assert(EW % 4 == 0 && UW % 4 == 0 && (COLS == 32 || COLS == 64), "warps");
   static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -241,8 +250,8 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]
 // tokens, 8192 x 22016: 1340 us, against 1420 with the buffer kept to the end).
 // TMEM is read in pieces of 16 lanes.  A warp of 64 tokens reads 16 columns at a
 // time with the next piece on the way while it folds one (1295 us); one of 32
-// tokens has two layers' sums or few pieces, and is faster with 32 columns at a
-// time (gated, 2048 tokens, 22016 x 8192: 1625 us against 1685).  The conversion
+// tokens has few pieces and is faster with 32 columns at a time (61 tokens, 8192 x
+// 8192 in groups of 32: 51.8 us against 53.0).  The conversion
 // to fp32 is an instruction of half the adders' rate; the add of 1.5 * 2^23 and
 // its subtraction would cost as much and more issue slots.
 template <int COLS, class Read>
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                   const __grid_constant__ CUtensorMap tmap_w1,
                   const __grid_constant__ CUtensorMap tmap_x, const Tiled a) {
-  constexpr int NL = C::NL, TN = C::TN, S = C::S, AS = C::AS, NU = C::NU, NS = C::NS, EW = C::EW,
+  constexpr int NL = C::NL, TN = C::TN, S = C::S, AS = C::AS, NU = C::NU, NB = C::NB, NS = C::NS, EW = C::EW,
                 UW = C::UW;
   constexpr uint32_t IDESC = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(TN >> 3) << 17) |
                              (uint32_t(BM >> 4) << 24);  // s32 += s8 x s8, both K-major
@@ -300,7 +309,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   float* swb = sx + C::SX_BYTES / 4;
   uint32_t* zb = reinterpret_cast<uint32_t*>(swb + C::SW_BYTES / 4);
   uint32_t* tops = zb + C::Z_BYTES / 4;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES);
+  uint64_t* trade = reinterpret_cast<uint64_t*>(tops + C::TOP_BYTES / 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(tops) + C::TOP_BYTES + C::TRADE_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * S, afull0 = empty0 + 8u * S,
@@ -310,9 +320,10 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 
   // Each chunk's last run closes its TMEM buffer, or runs span chunks.  Where
   // they close, two MMA warps take the operand slots in turn, provided that
-  // they use different buffers (their waits tell phases by parity alone).
+  // they use different buffers (their waits tell phases by parity alone):
+  // each layer has its own.
   const bool every = p.xgroups != 1 || a.runs != 1 || p.group == CH;
-  const bool turns = every && NU % (2 * a.runs) == 0;
+  const bool turns = every && (NL == 2 || NU % (2 * a.runs) == 0);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool leader = elect_one();
   if (threadIdx.x == 0) {
@@ -326,7 +337,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     }
     for (int u = 0; u < NU; ++u) {
       mbar_init(tfull0 + 8u * u, 1);
-      mbar_init(tempty0 + 8u * u, EW);
+      mbar_init(tempty0 + 8u * u, C::HALVES ? EW / 2 : EW);
     }
     for (int u = 0; u < C::NS; ++u) {
       mbar_init(sfull0 + 8u * u, 64);  // the scale warp's lanes and their copies
@@ -410,7 +421,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       // ----------------------------------------------------------- MMA warps
       const uint32_t mw = warp - (UW + EW + 1);
       const uint64_t DESC = smem_desc_sw128(0, 16, 1024);  // addresses are added
-      uint32_t st = 0, k = 0, unit = 0;  // stage, slots and TMEM buffers so far
+      uint32_t st = 0, k = 0, unit = 0;  // stage, slots and a layer's TMEM buffers so far
       bool open = false;                 // the current buffers hold a started run
       for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
         for (int c = c0; c < c1 && ok; ++c) {
@@ -427,8 +438,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
             // 32 columns are 32 bytes: 2 units of a descriptor's address
             if (a.runs == 1) {
-              const uint32_t u = unit + l, buf = u % NU, d = tmem_base + buf * TN;
-              if (!open) W4T_WAIT(tempty0 + 8u * buf, ((u / NU) & 1u) ^ 1u);
+              const uint32_t buf = l * NB + unit % NB, d = tmem_base + buf * TN;
+              if (!open) W4T_WAIT(tempty0 + 8u * buf, ((unit / NB) & 1u) ^ 1u);
               tc_fence_after();
               if (ok && leader) {
 #pragma unroll
@@ -437,8 +448,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
               }
             } else {
               for (int m = 0; m < a.runs; ++m) {
-                const uint32_t u = unit + l * a.runs + m, buf = u % NU, d = tmem_base + buf * TN;
-                W4T_WAIT(tempty0 + 8u * buf, ((u / NU) & 1u) ^ 1u);
+                const uint32_t u = unit + m, buf = l * NB + u % NB, d = tmem_base + buf * TN;
+                W4T_WAIT(tempty0 + 8u * buf, ((u / NB) & 1u) ^ 1u);
                 tc_fence_after();
                 if (ok && leader) {
                   if (a.runs == 2) {
@@ -460,7 +471,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           }
           if ((c & 1) && ++st == S) st = 0;
           open = !close;
-          if (close) unit += NL * a.runs;
+          if (close) unit += a.runs;
         }
       }
       if (!ok && leader) {  // given up: the tensor cores are done before TMEM is freed
@@ -600,7 +611,10 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     // ------------------------------------------------------------ epilogue
     W4T_MORE();
     const int e = threadIdx.x - UW * 32;
-    const int quarter = warp & 3, half = (warp - UW) >> 2;
+    const int quarter = warp & 3, half = (warp - UW) >> 2;  // of the rows, of the columns
+    // while folding: the columns, and with HALVES the only layer
+    constexpr int FCOLS = C::FCOLS, FL = C::HALVES ? 1 : NL;
+    const int fhalf = C::HALVES ? half >> 1 : half, mine = C::HALVES ? half & 1 : 0;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     constexpr int COLS = C::COLS;
     const int per_set = 4 / a.runs;
@@ -609,16 +623,16 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       const int row0 = static_cast<int>(t / a.tok_tiles) * BM;
       const int64_t tok0 = (t % a.tok_tiles) * TN;
       const int row_t = quarter * 32 + (lane >> 2);  // + 8 i + 16 h
-      Share<COLS> acc[NL];
+      Share<FCOLS> sum[FL];
 #pragma unroll
-      for (int l = 0; l < NL; ++l)
+      for (int l = 0; l < FL; ++l)
 #pragma unroll
-        for (int j = 0; j < COLS / 2; ++j) acc[l].v[j] = 0ull;
+        for (int j = 0; j < FCOLS / 2; ++j) sum[l].v[j] = 0ull;
       for (int cs = c0; cs < c1; cs += per_set, ++set) {
         const uint32_t at = set % NS;
         W4T_WAIT(sfull0 + 8u * at, (set / NS) & 1u);
-        const float* sxs = sx + (at * TN + half * COLS) * 4;
-        const float* sws = swb + (at * NL * BM + row_t) * 4;
+        const float* sxs = sx + (at * TN + fhalf * FCOLS) * 4;
+        const float* sws = swb + ((at * NL + mine) * BM + row_t) * 4;
         const int ce = min(cs + per_set, c1);
 #pragma unroll 1
         for (int c = cs; c < ce; ++c, ++sxs) {
@@ -626,27 +640,59 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 #pragma unroll 1
           for (int m = 0; m < a.runs; ++m) {
 #pragma unroll
-            for (int l = 0; l < NL; ++l) {
-              const uint32_t u = unit + l * a.runs + m, buf = u % NU;
+            for (int l = 0; l < FL; ++l) {
+              const uint32_t u = unit + m, buf = (mine + l) * NB + u % NB;
               const float* from = sws + l * BM * 4 + (c - cs) * a.runs + m;
               const float sw[4] = {from[0], from[32], from[64], from[96]};  // rows + 8 i + 16 h
-              W4T_WAIT(tfull0 + 8u * buf, (u / NU) & 1u);
+              W4T_WAIT(tfull0 + 8u * buf, (u / NB) & 1u);
               __syncwarp();  // the loads are the whole warp's, also after a wait that gave up
               tc_fence_after();
-              fold_run<COLS>(
-                  acc[l], tmem_base + lanes + buf * TN + half * COLS, sw, sxs, [&] {
+              fold_run<FCOLS>(
+                  sum[l], tmem_base + lanes + buf * TN + fhalf * FCOLS, sw, sxs, [&] {
                     tc_fence_before();
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(tempty0 + 8u * buf);
                   });
             }
           }
-          unit += NL * a.runs;
+          unit += a.runs;
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(sempty0 + 8u * at);
       }
       const int col_t = 2 * (lane & 3);
+      Share<COLS> acc[NL];
+      if constexpr (C::HALVES) {
+        // Of 2 COLS columns the warp keeps those of its half and gets their other
+        // layer's from the warp beside it, which lies in the same lanes, a quarter
+        // of its registers at a time.
+        uint64_t* to = trade + (warp - UW) * 128 + lane;
+        const uint64_t* from = trade + ((warp - UW) ^ 4) * 128 + lane;
+        const int bar = 2 + quarter + 4 * fhalf;
+#pragma unroll
+        for (int c = 0; c < COLS / 8; ++c) {  // eight columns: two registers for each 16 rows
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int low = ((j >> 1) * (FCOLS / 8) + c) * 2 + (j & 1), high = low + COLS / 4;
+            to[32 * j] = mine ? sum[0].v[low] : sum[0].v[high];
+          }
+          named_bar(bar, 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int low = ((j >> 1) * (FCOLS / 8) + c) * 2 + (j & 1), high = low + COLS / 4;
+            const int at = ((j >> 1) * (COLS / 8) + c) * 2 + (j & 1);
+            const uint64_t own = mine ? sum[0].v[high] : sum[0].v[low], other = from[32 * j];
+            acc[0].v[at] = mine ? other : own;
+            acc[NL - 1].v[at] = mine ? own : other;
+          }
+          named_bar(bar, 64);
+        }
+      } else {
+#pragma unroll
+        for (int l = 0; l < NL; ++l)
+#pragma unroll
+          for (int j = 0; j < COLS / 2; ++j) acc[l].v[j] = sum[l].v[j];
+      }
       if constexpr (C::BIG) {
         const bool codes = NL == 2 && p.out == w4a8::OUT_I8;
         if (NL == 2) {
