@@ -27,8 +27,7 @@
 //
 // Three shapes (Cfg).  SMALL and MID have one tile a cluster of up to 8 CTAs
 // that split the chunks; their sums meet in shared memory of the cluster, in
-// rank order, so the result does not vary.  BIG is persistent, without a split;
-// for the gated pair half of its epilogue warps has gate, half has up.
+// rank order, so the result does not vary.  BIG is persistent, without a split.
 //
 // What bounds it (measured): 4096 tokens through 8192 x 22016 (groups of 128)
 // take 1.29 ms, 1.15 PFLOP/s, 0.70 of the bf16 rate that cuBLAS reaches.  The
@@ -76,10 +75,12 @@ struct Cfg {
   static constexpr int COLS = TN / (EW / 4);         // columns (tokens) per epilogue warp
   // While it folds, half of the warps has gate, half has up, twice the columns
   // each, so that two chains of waits run beside each other and the reads of TMEM
-  // run ahead; they trade halves at the end of a tile (333 tokens, 11008 x 4096 in
-  // groups of 32: 245 us against 336; 2048 tokens, 22016 x 8192: 1589 against 1620).
-  static constexpr bool HALVES = BIG && NL == 2;
-  static constexpr int FCOLS = HALVES ? 2 * COLS : COLS;
+  // run ahead (333 tokens, 11008 x 4096 in groups of 32: 245 us, together 336; 60
+  // tokens, 22016 x 8192: 151 against 157; 2048 tokens: 1589 against 1620).  With
+  // four warps or one layer, crews for every other run were slower (61 tokens, 4096
+  // x 11008 in groups of 64: 27.0 us against 26.0).
+  static constexpr int CREWS = NL == 2 && EW > 4 ? 2 : 1;
+  static constexpr int FCOLS = CREWS * COLS;         // columns that a crew's warp folds
   static constexpr int X_BYTES = TN * CH;
   static constexpr int STAGE_BYTES = NL * PACKED_BYTES + 2 * X_BYTES;
   static constexpr int RING_BYTES = S * STAGE_BYTES;
@@ -88,13 +89,13 @@ struct Cfg {
   static constexpr int SW_BYTES = NS * 4 * NL * BM * 4;  // of row scales, four a row
   static constexpr int Z_BYTES = NS * NL * BM * 4;       // of zero points, four in a word
   static constexpr int TOP_BYTES = BIG && NL == 2 ? 4 * TN * 4 : 0;
-  static constexpr int TRADE_BYTES = HALVES ? EW * 1024 : 0;
+  static constexpr int TRADE_BYTES = BIG && CREWS == 2 ? EW * 1024 : 0;
   static constexpr int BARS = 2 * S + 2 * AS + 2 * NU + 2 * NS + 2;
   static constexpr int SMEM = RING_BYTES + AS * SLOT_BYTES + SX_BYTES + SW_BYTES + Z_BYTES + TOP_BYTES + TRADE_BYTES +
                               BARS * 8 + 16 + 1024 /* alignment */;
   static_assert(NB >= 1 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
-  static_assert(EW % 4 == 0 && UW % 4 == 0 && (COLS == 32 || COLS == 64), "warps");
+  static_assert(EW % 4 == 0 && UW % 4 == 0 && (FCOLS == 32 || FCOLS == 64), "warps");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // one CTA an SM, so no CTA of a cluster waits for TMEM that another holds
   static_assert(2 * SMEM > 228 * 1024, "one CTA");
@@ -337,7 +338,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     }
     for (int u = 0; u < NU; ++u) {
       mbar_init(tfull0 + 8u * u, 1);
-      mbar_init(tempty0 + 8u * u, C::HALVES ? EW / 2 : EW);
+      mbar_init(tempty0 + 8u * u, EW / C::CREWS);
     }
     for (int u = 0; u < C::NS; ++u) {
       mbar_init(sfull0 + 8u * u, 64);  // the scale warp's lanes and their copies
@@ -612,11 +613,11 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     W4T_MORE();
     const int e = threadIdx.x - UW * 32;
     const int quarter = warp & 3, half = (warp - UW) >> 2;  // of the rows, of the columns
-    // while folding: the columns, and with HALVES the only layer
-    constexpr int FCOLS = C::FCOLS, FL = C::HALVES ? 1 : NL;
-    const int fhalf = C::HALVES ? half >> 1 : half, mine = C::HALVES ? half & 1 : 0;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     constexpr int COLS = C::COLS;
+    // while folding: the columns, and the first layer
+    constexpr int FCOLS = C::FCOLS, FL = C::CREWS == 2 ? 1 : NL;
+    const int fhalf = half / C::CREWS, mine = half % C::CREWS;
     const int per_set = 4 / a.runs;
     uint32_t unit = 0, set = 0;
     for (int64_t t = tile0; t < tiles; t += tile_step) {
@@ -661,39 +662,39 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
         if (ok && lane == 0) mbar_arrive(sempty0 + 8u * at);
       }
       const int col_t = 2 * (lane & 3);
-      Share<COLS> acc[NL];
-      if constexpr (C::HALVES) {
-        // Of 2 COLS columns the warp keeps those of its half and gets their other
-        // layer's from the warp beside it, which lies in the same lanes, a quarter
-        // of its registers at a time.
-        uint64_t* to = trade + (warp - UW) * 128 + lane;
-        const uint64_t* from = trade + ((warp - UW) ^ 4) * 128 + lane;
-        const int bar = 2 + quarter + 4 * fhalf;
-#pragma unroll
-        for (int c = 0; c < COLS / 8; ++c) {  // eight columns: two registers for each 16 rows
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int low = ((j >> 1) * (FCOLS / 8) + c) * 2 + (j & 1), high = low + COLS / 4;
-            to[32 * j] = mine ? sum[0].v[low] : sum[0].v[high];
-          }
-          named_bar(bar, 64);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int low = ((j >> 1) * (FCOLS / 8) + c) * 2 + (j & 1), high = low + COLS / 4;
-            const int at = ((j >> 1) * (COLS / 8) + c) * 2 + (j & 1);
-            const uint64_t own = mine ? sum[0].v[high] : sum[0].v[low], other = from[32 * j];
-            acc[0].v[at] = mine ? other : own;
-            acc[NL - 1].v[at] = mine ? own : other;
-          }
-          named_bar(bar, 64);
-        }
-      } else {
-#pragma unroll
-        for (int l = 0; l < NL; ++l)
-#pragma unroll
-          for (int j = 0; j < COLS / 2; ++j) acc[l].v[j] = sum[l].v[j];
-      }
       if constexpr (C::BIG) {
+        Share<COLS> acc[NL];
+        if constexpr (C::CREWS == 2) {
+          // Of 2 COLS columns the warp keeps those of its half and gets their other
+          // layer's from the warp beside it, which lies in the same lanes, a quarter
+          // of its registers at a time.
+          uint64_t* to = trade + (warp - UW) * 128 + lane;
+          const uint64_t* from = trade + ((warp - UW) ^ 4) * 128 + lane;
+          const int bar = 2 + quarter + 4 * fhalf;
+#pragma unroll
+          for (int c = 0; c < COLS / 8; ++c) {  // eight columns: two registers for each 16 rows
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int low = ((j >> 1) * (FCOLS / 8) + c) * 2 + (j & 1), high = low + COLS / 4;
+              to[32 * j] = mine ? sum[0].v[low] : sum[0].v[high];
+            }
+            named_bar(bar, 64);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int low = ((j >> 1) * (FCOLS / 8) + c) * 2 + (j & 1), high = low + COLS / 4;
+              const int at = ((j >> 1) * (COLS / 8) + c) * 2 + (j & 1);
+              const uint64_t own = mine ? sum[0].v[high] : sum[0].v[low], other = from[32 * j];
+              acc[0].v[at] = mine ? other : own;
+              acc[NL - 1].v[at] = mine ? own : other;
+            }
+            named_bar(bar, 64);
+          }
+        } else {
+#pragma unroll
+          for (int l = 0; l < NL; ++l)
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) acc[l].v[j] = sum[l].v[j];
+        }
         const bool codes = NL == 2 && p.out == w4a8::OUT_I8;
         if (NL == 2) {
 #pragma unroll
@@ -752,14 +753,15 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
         named_bar(1, EW * 32);
         float* sums = reinterpret_cast<float*>(base);
 #pragma unroll
-        for (int l = 0; l < NL; ++l)
+        for (int l = 0; l < FL; ++l)
 #pragma unroll
-          for (int q = 0; q < COLS / 8; ++q)
+          for (int q = 0; q < FCOLS / 8; ++q)
 #pragma unroll
             for (int e2 = 0; e2 < 2; ++e2) {
-              float* to = sums + (l * TN + half * COLS + 8 * q + col_t + e2) * SUM_PITCH + row_t;
+              float* to =
+                  sums + ((mine + l) * TN + fhalf * FCOLS + 8 * q + col_t + e2) * SUM_PITCH + row_t;
 #pragma unroll
-              for (int hi = 0; hi < 4; ++hi) to[8 * hi] = acc[l].at(q, hi >> 1, hi & 1, e2);
+              for (int hi = 0; hi < 4; ++hi) to[8 * hi] = sum[l].at(q, hi >> 1, hi & 1, e2);
             }
       }
     }
