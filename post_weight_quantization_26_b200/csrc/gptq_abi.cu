@@ -78,6 +78,7 @@ constexpr int kEvents = 10;  // fork, join, 4 block-step and 4 trailing-update e
 struct DeviceInfo {
   bool ready = false;
   int num_sms = 0;
+  int clusters[9] = {};  // of that many CTAs, one an SM, that are on the GPU at once
   // The column sweep runs the block steps on the caller's stream and the
   // trailing updates on this auxiliary stream, joined by events; qmu keeps
   // calls from several host threads from interleaving on them.
@@ -109,6 +110,24 @@ cudaError_t allow_smem(F* f, int bytes) {
 template <class C>
 cudaError_t w4a8_allow_smem() {
   return allow_smem(w4a8t::w4a8_tiled_kernel<C>, C::SMEM);
+}
+template <class C>
+cudaError_t w4a8_clusters(int num_sms, int (&clusters)[9]) {
+  for (int k = 1; k <= 8; ++k) {
+    cudaLaunchConfig_t lc{};
+    cudaLaunchAttribute at[1];
+    lc.gridDim = dim3(static_cast<unsigned>(k * num_sms));
+    lc.blockDim = dim3(C::THREADS);
+    lc.dynamicSmemBytes = C::SMEM;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = k;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[k], w4a8t::w4a8_tiled_kernel<C>, &lc);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 template <class C>
 cudaError_t w4a8_allow_rows_shape() {
@@ -163,6 +182,7 @@ gptq_status device_setup(int* num_sms) {
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Small>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Mid>());
     GPTQ_CUDA_TRY(w4a8_allow_smem<W4a8Cfg<true>::Big>());
+    GPTQ_CUDA_TRY(w4a8_clusters<W4a8Cfg<false>::Small>(di.num_sms, di.clusters));
     GPTQ_CUDA_TRY(cudaFuncSetAttribute(syrk::syrk_bf16_tcgen05_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        syrk::SMEM_BYTES));
@@ -737,12 +757,17 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   a.wait_ns = g_wait_ns.load();
   a.ksplit = 1;
   if (!C::BIG) {
-    // The split that ends first: rounds of CTAs, each its chunks and a ramp
-    // worth about six chunks (launch, first loads, the sums' exchange).
-    const int64_t slots = static_cast<int64_t>(num_sms);
+    // The split that ends first: rounds of clusters, each the longest share of
+    // its chunks and a ramp (launch, first loads, the sums' exchange) of 7 us, which
+    // is worth 10, 7 or 4 chunks of 1, 2 or 4 runs.  61 tokens: 22016 x 8192 in two
+    // 70 us, whole 78, in four 89; 11008 x 4096 in groups of 32 in three 46.5 us,
+    // whole 51; 4096 x 11008 in four 19.6 us, in two 29.
+    const DeviceInfo* di = current_device_info();
+    const int quads = (nchunks + 3) / 4, ramp = a.runs == 1 ? 10 : a.runs == 2 ? 7 : 4;
     int64_t best = INT64_MAX;
-    for (int k = 1; k <= 8 && k <= (nchunks + 3) / 4; k *= 2) {
-      const int64_t cost = ((tiles * k + slots - 1) / slots) * ((nchunks + k - 1) / k + 6);
+    for (int k = 1; k <= 8 && k <= quads; ++k) {
+      const int64_t at_once = std::max(di ? di->clusters[k] : num_sms / k, 1);
+      const int64_t cost = ((tiles + at_once - 1) / at_once) * (4 * ((quads + k - 1) / k) + ramp);
       if (cost < best) { best = cost; a.ksplit = k; }
     }
   }
