@@ -151,7 +151,7 @@ struct Raw8 {
 
 // Aligned rows of whole vectors of eight: a block a token, NV vectors a thread
 // in registers, so the pass reads and writes each byte once and is bound by
-// HBM: 16384 x 8192 bf16 with residual, 939 MB, in 176 us, 5.3 TB/s.  A block
+// HBM: 16384 x 8192 bf16 with residual, 939 MB, in 172 us, 5.5 TB/s.  A block
 // takes rows blockIdx.x, + gridDim.x, ... and has the next row's loads on the way
 // while it reduces and writes the current one (AHEAD; 205 us with a block a row).
 // Rows of more than 8192 columns take more threads, and then the registers do not

@@ -34,9 +34,9 @@
 // MMAs would take 512 clocks a chunk of 128 x 256 outputs; with nothing but
 // copies, unpacking and MMAs a chunk takes 860, with the epilogue 1750: scaling
 // each run's sums costs a conversion, a product and a fused add an output, 512
-// clocks of each pipe, in chains that sixteen warps do not fully overlap.  More
-// epilogue warps in groups of their own, spreading the token scales by an MMA
-// with ones, and 128-token tiles were built and were slower.
+// clocks of each pipe, in chains that sixteen warps do not fully overlap.  For
+// one layer more epilogue warps in groups of their own, and spreading the token
+// scales by an MMA with ones and 128-token tiles, were built and were slower.
 #pragma once
 
 #include <cooperative_groups.h>
