@@ -95,6 +95,15 @@ struct Cfg {
                               BARS * 8 + 16 + 1024 /* alignment */;
   static_assert(NB >= 1 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM");
   static_assert(SUM_BYTES <= RING_BYTES + AS * SLOT_BYTES, "the sums lie over the ring");
+  // Where two MMA warps (and two groups of unpack warps) take the slots in turn, an
+  // odd number of slots hands a slot from one to the other, and a wait by parity
+  // takes a barrier that is a whole phase behind for its own.  MMA warps: a warp has
+  // waited for the TMEM buffer of its chunk first, which is free when the chunk NB
+  // before is folded; folds go in order, so with NB <= AS the slot's chunk before this
+  // one is multiplied.  Unpack groups: the stage's words came after the MMAs of the
+  // stage S before, and a warp's commit stands for its earlier MMAs, too; with S <= 3
+  // those of 2 AS chunks before are among them.
+  static_assert(AS % 2 == 0 || (NL == 1 && NB <= AS && AS == 3 && S <= 3), "slots by parity");
   static_assert(EW % 4 == 0 && UW % 4 == 0 && (FCOLS == 32 || FCOLS == 64), "warps");
   static_assert(SMEM <= 227 * 1024, "shared memory");
   // one CTA an SM, so no CTA of a cluster waits for TMEM that another holds
@@ -322,7 +331,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   // Each chunk's last run closes its TMEM buffer, or runs span chunks.  Where
   // they close, two MMA warps take the operand slots in turn, provided that
   // they use different buffers (their waits tell phases by parity alone):
-  // each layer has its own.
+  // each layer has its own.  For the slots themselves see Cfg.
   const bool every = p.xgroups != 1 || a.runs != 1 || p.group == CH;
   const bool turns = every && (NL == 2 || NU % (2 * a.runs) == 0);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -436,11 +445,12 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (turns ? (k & 1u) != mw : mw != 0) continue;
             const uint32_t slot = k % AS;
             const uint64_t ad = DESC + ((slots + slot * SLOT_BYTES) >> 4);
-            W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
             // 32 columns are 32 bytes: 2 units of a descriptor's address
             if (a.runs == 1) {
               const uint32_t buf = l * NB + unit % NB, d = tmem_base + buf * TN;
+              // the buffer before the slot: the slot's parity means nothing before
               if (!open) W4T_WAIT(tempty0 + 8u * buf, ((unit / NB) & 1u) ^ 1u);
+              W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
               tc_fence_after();
               if (ok && leader) {
 #pragma unroll
@@ -448,6 +458,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                 if (close) mma_commit(tfull0 + 8u * buf);
               }
             } else {
+              W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
               for (int m = 0; m < a.runs; ++m) {
                 const uint32_t u = unit + m, buf = l * NB + u % NB, d = tmem_base + buf * TN;
                 W4T_WAIT(tempty0 + 8u * buf, ((u / NB) & 1u) ^ 1u);
