@@ -435,15 +435,26 @@ gptq_status gptq_device_status(void* stream);
  *                 kernel issues no loads, so the MMA thread's first bounded
  *                 wait runs out; GPTQ_FAULT_TRAILING_STALL: the same in the
  *                 trailing-update kernel of gptq_quantize_layer and
- *                 gptq_awq_search.  Nothing is in flight when the waits give
- *                 up; the kernel records GPTQ_ERR_TIMEOUT, frees its tensor
- *                 memory and returns, and the context stays usable.  The
- *                 outputs of a stalled call are meaningless.
+ *                 gptq_awq_search; GPTQ_FAULT_W4A8_LOADS: the same in the
+ *                 kernels of gptq_w4a8_matmul and gptq_w4a8_gated;
+ *                 GPTQ_FAULT_W4A8_STAGES: there, no stage of the producer's
+ *                 ring counts as read, so that its own wait runs out (where
+ *                 there is more than the ring holds).  No load or product is
+ *                 in flight when the kernel returns; the kernel records
+ *                 GPTQ_ERR_TIMEOUT, frees its tensor memory and returns, and
+ *                 the context stays usable.  The outputs of a stalled call are
+ *                 meaningless.
  *  wait_limit_ns  the limit of every bounded wait in every kernel, 1 ms to
  *                 10 s; 0 restores the default of 2 s.
  * Returns GPTQ_ERR_INVALID for other values (nothing changes then).  Not
  * thread-safe against launches in flight on other host threads. */
-enum { GPTQ_FAULT_NONE = 0, GPTQ_FAULT_SYRK_STALL = 1, GPTQ_FAULT_TRAILING_STALL = 2 };
+enum {
+  GPTQ_FAULT_NONE = 0,
+  GPTQ_FAULT_SYRK_STALL = 1,
+  GPTQ_FAULT_TRAILING_STALL = 2,
+  GPTQ_FAULT_W4A8_LOADS = 4,
+  GPTQ_FAULT_W4A8_STAGES = 5
+};
 gptq_status gptq_fault_inject(int where, int64_t wait_limit_ns);
 
 /* Number of kernels this library has launched in this process (all devices,

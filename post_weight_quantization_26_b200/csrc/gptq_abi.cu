@@ -630,6 +630,13 @@ bool w4a8_layer_ok(const uint32_t* qweight, const float* scales, const uint8_t* 
   return qweight && scales && zeros && aligned(qweight, 16) && aligned(scales, 4);
 }
 
+int w4a8_stall() {
+  const int fault = g_fault.load();
+  return fault == GPTQ_FAULT_W4A8_LOADS    ? w4a8::STALL_LOADS
+         : fault == GPTQ_FAULT_W4A8_STAGES ? w4a8::STALL_STAGES
+                                           : 0;
+}
+
 // 2-D byte matrix for TMA: rows of `inner` bytes, box bx x by.
 gptq_status encode_u8_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer,
                          uint64_t row_bytes, uint32_t bx, uint32_t by, CUtensorMapSwizzle swz) {
@@ -653,6 +660,7 @@ gptq_status w4a8_rows_launch(const w4a8::Params& p, int num_sms, cudaStream_t s)
   w4a8::Launch a{};
   a.p = p;
   a.wait_ns = g_wait_ns.load();
+  a.stall = w4a8_stall();
   a.whole = p.d_col % 128 == 0;
   CUtensorMap mw[2], mx;
   for (int l = 0; l < 2; ++l) {
@@ -755,6 +763,7 @@ gptq_status w4a8_tiled(const w4a8::Params& p, int num_sms, cudaStream_t s) {
   for (int l = 0; l < C::NL; ++l)
     a.wvec = a.wvec && aligned(p.layer[l].scales, 16) && aligned(p.layer[l].zeros, 4);
   a.wait_ns = g_wait_ns.load();
+  a.stall = w4a8_stall();
   a.ksplit = 1;
   if (!C::BIG) {
     // The split that ends first: rounds of clusters, each the longest share of
@@ -1076,7 +1085,8 @@ gptq_status gptq_hessian_accumulate_ordered(float* H, const void* X, int64_t n, 
 
 gptq_status gptq_fault_inject(int where, int64_t wait_limit_ns) {
   if (where != GPTQ_FAULT_NONE && where != GPTQ_FAULT_SYRK_STALL &&
-      where != GPTQ_FAULT_TRAILING_STALL)
+      where != GPTQ_FAULT_TRAILING_STALL && where != GPTQ_FAULT_W4A8_LOADS &&
+      where != GPTQ_FAULT_W4A8_STAGES)
     return GPTQ_ERR_INVALID;
   if (wait_limit_ns != 0 && (wait_limit_ns < 1000000 || wait_limit_ns > 10000000000ll))
     return GPTQ_ERR_INVALID;

@@ -43,6 +43,9 @@ namespace gptq {
 namespace w4a8 {
 
 constexpr int OUT_F32 = 0, OUT_BF16 = 1, OUT_I8 = 2;  // == GPTQ_F32, GPTQ_BF16, GPTQ_I8
+// Fault injection, here and in the tile kernel: the producer issues no loads, or
+// a stage of its ring is never counted as read, so that a wait runs out.
+constexpr int STALL_LOADS = 1, STALL_STAGES = 2;
 constexpr int WARPS = 8;     // computing warps
 constexpr int THREADS = WARPS * 32 + 32;  // and the producer warp
 constexpr int CPS = WARPS;      // 128-column chunks per stage
@@ -128,6 +131,7 @@ struct Launch {
   uint64_t wait_ns;
   int tiles;  // blocks of ROWS rows
   int whole;  // the tokens' map is 3-D: columns of a chunk, chunks, tokens
+  int stall;  // a STALL_* (0 in normal use)
 };
 
 template <class C>
@@ -151,7 +155,7 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, C::STAGED ? 33 : 1);  // the copies, and the producer's lanes'
-      mbar_init(empty0 + 8u * s, WARPS);
+      mbar_init(empty0 + 8u * s, WARPS + (a.stall == STALL_STAGES));
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -173,7 +177,7 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   if (warp == WARPS) {
     // ------------------------------------------------------------ producer
     uint32_t issued = 0;
-    for (int tile = blockIdx.x; tile < a.tiles && ok; tile += gridDim.x) {
+    for (int tile = blockIdx.x; tile < a.tiles && ok && a.stall != STALL_LOADS; tile += gridDim.x) {
       const int row0 = tile * ROWS;
       for (int s = 0; s < stages; ++s) {
         ok = mbar_wait_bounded(empty0 + 8u * st, ph ^ 1u, abort_flag, a.wait_ns);

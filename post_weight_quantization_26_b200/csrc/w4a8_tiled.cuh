@@ -122,6 +122,7 @@ struct Tiled {
   int yvec;          // eight rows of an output are aligned for one store
   int xvec, wvec;    // rows of token scales, and of row scales and zero points, allow vector loads
   uint64_t wait_ns;
+  int stall;         // a w4a8::STALL_* (0 in normal use)
 };
 
 __device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -339,7 +340,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full0 + 8u * s, 1);
-      mbar_init(empty0 + 8u * s, 8 * NL + (turns ? 2 : 1));  // unpacked, and multiplied
+      mbar_init(empty0 + 8u * s, 8 * NL + (turns ? 2 : 1) +  // unpacked, and multiplied
+                                     (a.stall == w4a8::STALL_STAGES));
     }
     for (int s = 0; s < AS; ++s) {
       mbar_init(afull0 + 8u * s, 4);
@@ -390,6 +392,11 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
   bool ok = true;
 #define W4T_WAIT(bar, par) \
   (ok = ok && mbar_wait_bounded((bar), (par), abort_flag, a.wait_ns))
+// The same with one answer for the warp, whose lanes leave loops by it and meet
+// again inside them: where one lane gave up and another's wait came through, those
+// that stay would wait for those that left.  (The other roles keep looping.)
+#define W4T_WAIT_ALL(bar, par) \
+  (ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded((bar), (par), abort_flag, a.wait_ns)))
 
 #define W4T_FEWER() \
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEWER))
@@ -402,11 +409,11 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       // ------------------------------------------------------------ TMA warp
       // The warp stays together and one thread issues, here and below.
       uint32_t st = 0, ph = 0, issued = 0;
-      for (int64_t t = tile0; t < tiles && ok; t += tile_step) {
+      for (int64_t t = tile0; t < tiles && ok && a.stall != w4a8::STALL_LOADS; t += tile_step) {
         const int row = static_cast<int>(t / a.tok_tiles) * BM;
         const int tok = static_cast<int>(t % a.tok_tiles) * TN;
         for (int c = c0; c < c1; c += 2) {
-          if (!W4T_WAIT(empty0 + 8u * st, ph ^ 1u)) break;
+          if (!W4T_WAIT_ALL(empty0 + 8u * st, ph ^ 1u)) break;
           const uint32_t fb = full0 + 8u * st, at = ring + st * C::STAGE_BYTES;
           if (leader) {
             mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
@@ -449,8 +456,8 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (a.runs == 1) {
               const uint32_t buf = l * NB + unit % NB, d = tmem_base + buf * TN;
               // the buffer before the slot: the slot's parity means nothing before
-              if (!open) W4T_WAIT(tempty0 + 8u * buf, ((unit / NB) & 1u) ^ 1u);
-              W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
+              if (!open) W4T_WAIT_ALL(tempty0 + 8u * buf, ((unit / NB) & 1u) ^ 1u);
+              W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
               tc_fence_after();
               if (ok && leader) {
 #pragma unroll
@@ -458,10 +465,10 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                 if (close) mma_commit(tfull0 + 8u * buf);
               }
             } else {
-              W4T_WAIT(afull0 + 8u * slot, (k / AS) & 1u);
+              W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
               for (int m = 0; m < a.runs; ++m) {
                 const uint32_t u = unit + m, buf = l * NB + u % NB, d = tmem_base + buf * TN;
-                W4T_WAIT(tempty0 + 8u * buf, ((u / NB) & 1u) ^ 1u);
+                W4T_WAIT_ALL(tempty0 + 8u * buf, ((u / NB) & 1u) ^ 1u);
                 tc_fence_after();
                 if (ok && leader) {
                   if (a.runs == 2) {
@@ -778,6 +785,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
     }
   }
 #undef W4T_WAIT
+#undef W4T_WAIT_ALL
 #undef W4T_FEWER
 #undef W4T_MORE
 

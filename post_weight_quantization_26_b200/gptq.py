@@ -33,6 +33,7 @@ NOALLOC_MAX_TILES = 65536  # GPTQ_NOALLOC_MAX_TILES in include/gptq.h
 ACT_GROUP = 128  # columns that share an activation scale, where a token has several
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.int8: 2}  # gptq_dtype in include/gptq.h
 FAULT_NONE, FAULT_SYRK_STALL, FAULT_TRAILING_STALL = 0, 1, 2  # GPTQ_FAULT_* in include/gptq.h
+FAULT_W4A8_LOADS, FAULT_W4A8_STAGES = 4, 5
 
 
 class GptqError(RuntimeError):
