@@ -227,7 +227,9 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok && lane == 0) {  // given up: no copy may land in memory that is handed on
+    // No copy may land in memory that is handed on.  Usually all have been read;
+    // not so where this warp or a reader, at its own time, gave up.
+    if (lane == 0) {
       int own = 0;
       for (uint32_t k = 0; k < S && k < issued; ++k) {
         const uint32_t i = issued - 1 - k;

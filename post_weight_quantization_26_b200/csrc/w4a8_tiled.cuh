@@ -427,7 +427,9 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           if (++st == S) { st = 0; ph ^= 1u; }
         }
       }
-      if (!ok && leader) {  // given up: no copy may land in memory that is handed on
+      // No copy may land in memory that is handed on.  Usually all have been read;
+      // not so where this role or a reader, at its own time, gave up.
+      if (leader) {
         int own = 0;
         for (uint32_t k = 0; k < S && k < issued; ++k) {
           const uint32_t i = issued - 1 - k;
@@ -493,7 +495,9 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
           if (close) unit += a.runs;
         }
       }
-      if (!ok && leader) {  // given up: the tensor cores are done before TMEM is freed
+      // The tensor cores are done before TMEM and the operands' memory are freed,
+      // whichever role gave up.
+      if (leader) {
         int own = 0;
         mma_commit(drain + 8u * mw);
         mbar_wait_bounded(drain + 8u * mw, 0, &own, a.wait_ns);
