@@ -454,12 +454,15 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
             if (turns ? (k & 1u) != mw : mw != 0) continue;
             const uint32_t slot = k % AS;
             const uint64_t ad = DESC + ((slots + slot * SLOT_BYTES) >> 4);
+            // An even number of slots: a warp sees its slots' every phase, and waits here
+            // (before the buffer; 2048 tokens gated, 22016 x 8192: 1608 us, after it
+            // 1648).  Odd: the slot's parity means nothing before the buffer is free.
+            if constexpr (AS % 2 == 0) W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
             // 32 columns are 32 bytes: 2 units of a descriptor's address
             if (a.runs == 1) {
               const uint32_t buf = l * NB + unit % NB, d = tmem_base + buf * TN;
-              // the buffer before the slot: the slot's parity means nothing before
               if (!open) W4T_WAIT_ALL(tempty0 + 8u * buf, ((unit / NB) & 1u) ^ 1u);
-              W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
+              if constexpr (AS % 2 != 0) W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
               tc_fence_after();
               if (ok && leader) {
 #pragma unroll
@@ -467,7 +470,7 @@ w4a8_tiled_kernel(const __grid_constant__ CUtensorMap tmap_w0,
                 if (close) mma_commit(tfull0 + 8u * buf);
               }
             } else {
-              W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
+              if constexpr (AS % 2 != 0) W4T_WAIT_ALL(afull0 + 8u * slot, (k / AS) & 1u);
               for (int m = 0; m < a.runs; ++m) {
                 const uint32_t u = unit + m, buf = l * NB + u % NB, d = tmem_base + buf * TN;
                 W4T_WAIT_ALL(tempty0 + 8u * buf, ((u / NB) & 1u) ^ 1u);

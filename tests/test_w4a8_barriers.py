@@ -38,11 +38,16 @@ def shapes():
     return out
 
 
-def order():
-    """Which of its two barriers an MMA warp waits for first where a chunk is one run."""
+def order(slots):
+    """Which of its two barriers an MMA warp waits for first where a chunk is one run,
+    with an even or odd number of slots."""
     text = open(os.path.join(CSRC, "w4a8_tiled.cuh")).read()
     text = text[text.index("- MMA warps\n"):text.index("- scale warp\n")]
-    return re.search(r"W4T_\w*WAIT\w*\((tempty|afull)0", text)[1]
+    for line in text.splitlines():
+        wait = re.search(r"W4T_\w*WAIT\w*\((tempty|afull)0", line)
+        only = re.search(r"if constexpr \(AS % 2 (==|!=) 0\)", line)
+        if wait and (not only or (only[1] == "==") == (slots % 2 == 0)):
+            return wait[1]
 
 
 class Wrong(Exception):
@@ -234,7 +239,7 @@ def test_every_order_of_events(name, nl, runs):
     # with one run a chunk every slot, stage and buffer comes round twice or more; more
     # runs and layers have more orders, and get as many chunks as seconds allow
     chunks = {(1, 1): 20, (1, 2): 10, (1, 4): 6, (2, 1): 8, (2, 2): 4, (2, 4): 2}[nl, runs]
-    visit(**shape, runs=runs, first=order(), chunks=chunks)
+    visit(**shape, runs=runs, first=order(shape["slots"]), chunks=chunks)
 
 
 def test_the_model_finds_a_parity_two_phases_back():
