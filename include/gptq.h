@@ -302,7 +302,9 @@ typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1, GPTQ_I8 = 2 } gptq_dtype;
  *   r = X + residual, rounded once to the residual's type and stored,
  *   y = r / sqrt(mean_k r_k^2 + eps) * weight,
  *   codes, scales = the 8-bit form of y above.
- * The norm is taken of the stored r.  All arithmetic is fp32.
+ * The norm is taken of the stored r.  All arithmetic is fp32, the squares,
+ * too: where their sum overflows (values near 2^64 / sqrt(d)) y, codes and
+ * scales are 0; where eps is 0 and they underflow (below 2^-63) y is inexact.
  *  X             n x d, row stride ldx, type x_type (GPTQ_F32 or GPTQ_BF16).
  *  residual      n x d, row stride ldr, type r_type (GPTQ_F32 or GPTQ_BF16),
  *                or NULL: r = X and residual_out is not written.
@@ -340,7 +342,8 @@ gptq_status gptq_rmsnorm_quant8(const void* X, int x_type, int64_t ldx, const vo
  * in fp32.  With runs of R = gcd(group_size, 128) columns, or 128 for
  * group_size 0, and m = ceil(d_col / R) of them,
  *   |Y - exact| <= (m + 16) 2^-24 sum over runs |s_x s sum_run x (q - z)|,
- * in whatever order the runs are added.  The result does not vary from call
+ * in whatever order the runs are added, as long as each s_x s and the sums are
+ * in fp32's normal range.  The result does not vary from call
  * to call; its last bits may vary with n, which decides how the sum is split.
  * 0 <= n <= 2^24 (n = 0 is a no-op).  Asynchronous; allocates nothing. */
 gptq_status gptq_w4a8_matmul(const uint32_t* qweight, const float* scales, const uint8_t* zeros,

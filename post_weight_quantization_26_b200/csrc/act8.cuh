@@ -6,8 +6,12 @@
 //
 // The norm is taken of the stored r, so a later reader of the residual
 // stream sees the values that the codes were made from.  Everything between
-// the loads and the stores is fp32; the sum of squares is a tree over the
-// block, so its error grows with the logarithm of the row.
+// the loads and the stores is fp32.  Of the sum of squares a thread adds its own
+// share in order, 8 to 32 columns with the row in registers and d / 256 in the
+// kernel for any width, and the threads' sums meet in a tree: a relative error of
+// at most (d / 256 + 42) 2^-24.  Squares outside fp32's range are lost: a token of
+// values near 2^64 / sqrt(d) and beyond gives scales 0, with eps 0 one below 2^-63
+// loses accuracy.
 //
 // Maxima are taken over the bit patterns of |y| as unsigned integers: they
 // order like the values, and every NaN lies above infinity, so a NaN is never
@@ -245,7 +249,8 @@ __global__ void __launch_bounds__(AHEAD ? 1024 / NV : 1024) rmsnorm_quant8_kerne
 }
 
 // Any width, stride and alignment: one block a token, three passes that read
-// r back from where it is (the caches).  A warp owns whole groups of 128
+// r back from where it is (the caches), an element at a time: 4096 x 4095 bf16 with
+// residual take 59 us, 2.0 TB/s (4096 columns, in registers: 24 us).  A warp owns whole groups of 128
 // columns, four a lane, and each element is only ever touched by one thread,
 // so res_out may be the memory of x or of the residual.
 template <typename TX, typename TR>

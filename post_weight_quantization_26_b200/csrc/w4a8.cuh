@@ -28,9 +28,9 @@
 // the way, and take tile after tile, so the copies never pause.  Scales and
 // zero points come with the stages by asynchronous copies of 16 bytes; where
 // groups or alignment do not allow that, they are loaded one chunk ahead.  One
-// token of 22016 x 8192: gate and up 42 us with the staged scales, 45 us with
-// loads (4600 GB/s, 0.70 of the memory's rate; the same loop without scales or
-// products, copies alone, 34 us); what is left is the chain of a stage, about
+// token of 22016 x 8192: gate and up 40 to 42 us with the staged scales (4600 to
+// 4860 GB/s, 0.71 to 0.74 of the memory's rate), 45 us with loads; the same loop
+// without scales or products, copies alone, 34 us.  What is left is the chain of a stage, about
 // a wait, the reads, 12 mma and their folds, on 16 warps an SM.
 #pragma once
 
@@ -103,7 +103,8 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
 
 // NL: layers; RJ: runs of 32 columns in a region: 1, 2, or 4 (whole chunks);
 // NT: groups of eight tokens; STAGED: scales come with the stages, for groups of
-// 32 RJ columns in fours and aligned rows; S: stages; MINB: CTAs per SM.
+// 32 RJ columns in fours and aligned rows.  Derived: S, the ring's stages, as many
+// as let MINB CTAs share an SM.
 template <int NL_, int RJ_, int NT_, bool STAGED_>
 struct Cfg {
   static constexpr int NL = NL_, RJ = RJ_, NT = NT_;
@@ -433,9 +434,9 @@ w4a8_rows_kernel(const __grid_constant__ CUtensorMap tmap_w0,
 
 // The 8-bit form of fp32 rows, a warp a token and block of 128 columns.  It
 // stands behind the row kernel on the stream, whose CTAs hold 16 rows of a
-// block each: clusters that exchange their maxima would have to lie within a
-// GPC, which leaves 33 of 37 room and a fifth of the SMs idle (61 us for one
-// token through a gated pair of 22016 x 8192 that takes 44 without).
+// block each: clusters of eight that exchange their maxima have to lie within a
+// GPC, where 33 fit on the GPU instead of 37 and a ninth of the places stays empty
+// (with them one token through a gated pair of 22016 x 8192 took 61 us, without 44).
 __global__ void __launch_bounds__(128) quant8_rows_kernel(const float* __restrict__ h, int64_t ldh,
                                                           int n, int d, int8_t* codes, int64_t ldq,
                                                           float* scales) {

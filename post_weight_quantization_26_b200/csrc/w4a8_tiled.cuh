@@ -30,11 +30,12 @@
 // rank order, so the result does not vary.  BIG is persistent, without a split.
 //
 // What bounds it (measured): 4096 tokens through 8192 x 22016 (groups of 128)
-// take 1.29 ms, 1.15 PFLOP/s, 0.70 of the bf16 rate that cuBLAS reaches.  The
+// take 1.27 to 1.30 ms, 1.16 PFLOP/s, 0.70 of the bf16 rate that cuBLAS reaches.  The
 // MMAs would take 512 clocks a chunk of 128 x 256 outputs; with nothing but
-// copies, unpacking and MMAs a chunk takes 860, with the epilogue 1750: scaling
-// each run's sums costs a conversion, a product and a fused add an output, 512
-// clocks of each pipe, in chains that sixteen warps do not fully overlap.  For
+// copies, unpacking and MMAs a chunk takes 860 (one scale a row and a token, whose
+// runs are folded once a tile: 0.82 ms), with the epilogue 1970: scaling
+// each run's sums costs a conversion, a product and a fused add an output, 2050 of
+// the chunk's 6160 warp instructions, with the issue slots 78% taken.  For
 // one layer more epilogue warps in groups of their own, and spreading the token
 // scales by an MMA with ones and 128-token tiles, were built and were slower.
 #pragma once
