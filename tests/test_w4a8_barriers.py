@@ -69,8 +69,9 @@ class Barrier:
         return (state[0] & 1) != (parity & 1)
 
 
-def visit(nl, ug, s, slots, nu, runs, first, chunks):
-    """Visits every interleaving; raises Wrong.  Every chunk's last run closes."""
+def visit(nl, ug, s, slots, nu, runs, first, chunks, parts=1):
+    """Visits every interleaving; raises Wrong.  Every chunk's last run closes.  `parts`:
+    warps of a group, each with its rows of a slot."""
     nb = nu // nl
     turns = nl == 2 or nu % (2 * runs) == 0
     stages = chunks // 2
@@ -85,8 +86,8 @@ def visit(nl, ug, s, slots, nu, runs, first, chunks):
     def buffer(k, m):
         return (k % nl) * nb + unit(k, m) % nb
 
-    unpack = [[(op, k) for k in range(total) if k % ug == g for op in ("full", "aempty", "write")]
-              for g in range(ug)]
+    unpack = [[(op, k) for k in range(total) if k % ug == g // parts
+               for op in ("full", "aempty", "write")] for g in range(ug * parts)]
     mma = []
     for w in range(2 if turns else 1):
         ops = []
@@ -109,18 +110,20 @@ def visit(nl, ug, s, slots, nu, runs, first, chunks):
              [("tfull", i) for i in range(nu)] + [("tempty", i) for i in range(nu)])
     index = {b: i for i, b in enumerate(names)}
     count = {b: 1 for b in names}
+    for i in range(slots):
+        count["afull", i] = parts
     for i in range(s):
-        count["empty", i] = 2 * nl + (2 if turns else 1)
+        count["empty", i] = 2 * nl * parts + (2 if turns else 1)
 
     def arrive(bars, name):
         i = index[name]
         bars[i] = Barrier.arrive(bars[i], count[name])
 
     # a state: copies issued; stages in flight; stage that each ring place holds;
-    # each unpacking group's place in its program; chunk that each slot holds; each
+    # each unpacking warp's place in its program; chunk that each slot's rows hold; each
     # MMA warp's place; its products done; product that each buffer holds; folds done
     # of each layer; barriers
-    start = (0, (), (-1,) * s, (0,) * ug, (-1,) * slots, (0,) * len(mma), (0,) * len(mma),
+    start = (0, (), (-1,) * s, (0,) * len(unpack), (-1,) * (slots * parts), (0,) * len(mma), (0,) * len(mma),
              (None,) * nu, (0,) * nl, ((0, None),) * len(names))
 
     def issued(w, place):
@@ -147,7 +150,7 @@ def visit(nl, ug, s, slots, nu, runs, first, chunks):
             arrive(b, ("full", j % s))
             yield (tma, tuple(i for i in flight if i != j), tuple(place), ups, held, ms, done, bufs,
                    fs, tuple(b))
-        for g in range(ug):
+        for g in range(len(unpack)):
             if ups[g] == len(unpack[g]):
                 continue
             op, k = unpack[g][ups[g]]
@@ -165,7 +168,7 @@ def visit(nl, ug, s, slots, nu, runs, first, chunks):
                 if any(r % slots == slot for _, r, _ in reading(state)):
                     raise Wrong("a slot written while it is read")
                 h, b = list(held), list(bars)
-                h[slot] = k
+                h[slot * parts + g % parts] = k
                 arrive(b, ("afull", slot))
                 arrive(b, ("empty", j % s))
             at = list(ups)
@@ -180,7 +183,8 @@ def visit(nl, ug, s, slots, nu, runs, first, chunks):
                 elif op == "tempty":
                     ok = Barrier.passes(bars[index["tempty", buffer(k, m)]], (unit(k, m) // nb) ^ 1)
                 else:
-                    if held[k % slots] != k or ring[chunk(k) // 2 % s] != chunk(k) // 2:
+                    rows = held[k % slots * parts:(k % slots + 1) * parts]
+                    if rows != (k,) * parts or ring[chunk(k) // 2 % s] != chunk(k) // 2:
                         raise Wrong("a product of another chunk's operands")
                     before = unit(k, m) - nb
                     if before >= 0 and fs[k % nl] <= before:
@@ -240,6 +244,13 @@ def test_every_order_of_events(name, nl, runs):
     # runs and layers have more orders, and get as many chunks as seconds allow
     chunks = {(1, 1): 20, (1, 2): 10, (1, 4): 6, (2, 1): 8, (2, 2): 4, (2, 4): 2}[nl, runs]
     visit(**shape, runs=runs, first=order(shape["slots"]), chunks=chunks)
+
+
+def test_warps_of_a_group_apart():
+    """The shape whose slots change hands, with the warps of each unpacking group
+    ahead of one another."""
+    shape = shapes()["Big", 1]
+    visit(**shape, runs=1, first=order(shape["slots"]), chunks=12, parts=2)
 
 
 def test_the_model_finds_a_parity_two_phases_back():
